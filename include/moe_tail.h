@@ -404,6 +404,131 @@ int moe_tail_selftest_wait_timeout(unsigned int limit_us, void* stream);
  * Returns MOE_TAIL_EINVAL for a limit above 1 s. */
 int moe_tail_set_stage_wait_limit(unsigned long long limit_ns);
 
+/*
+ * ---- The expert layer around the tail (no counterpart on the pages) ----------
+ *
+ * What a layer with 8-bit experts does before and after the finalize calls:
+ * residual addition, norm and 8-bit rows; routes sorted by expert and rows
+ * copied into that order; the experts' 8-bit products; silu(gate) * up in
+ * 8-bit rows between the two; and the weighted sum back, with the gradients.
+ * moe_tail_sort_routes' permuted_idx is the finalize calls' permuted_idx (one
+ * slot) and the product's out their rows.  The conventions above hold.
+ *
+ * Rows in 8 bits: q [rows][width], int8 or e4m3 per q_dtype (MOE_TAIL_Q_*),
+ * with FP32 scales per group: the whole row (group = 0, scale [rows]) or 128
+ * columns (group = 128, scale [rows][ceil(width / 128)], the last group
+ * shorter).  A value is q * scale.  With M = 127 (int8) or 448 (e4m3):
+ *   scale = max|y| / M,  q = round(y / scale), to nearest even, |q| <= M
+ * A group of zeros has scale 0 and q = 0; a group with a NaN or an infinity
+ * has scale NaN and q = 0, so that what is computed from it is NaN.
+ */
+enum { MOE_TAIL_Q_INT8 = 0, MOE_TAIL_Q_E4M3 = 1 };
+
+/*
+ * Residual addition, RMS norm and 8-bit rows.  Per row:
+ *   h = fp32(x) + fp32(residual)             (residual NULL: h = x)
+ *   residual_out = bf16(h)                   (unless NULL)
+ *   v = (h / sqrt(sum(h^2) * (1/H) + eps)) * (fp32(gamma) + gain_center)
+ *   y = bf16(v)                              (unless NULL)
+ *   q, scale = v in 8 bits (above)
+ * All in FP32 from h on: the norm is of h, not of its BF16 rounding.
+ *
+ *   x, residual, residual_out, y   BF16 [b][H]; residual_out may be x or
+ *                                  residual itself (in place)
+ *   gamma                          BF16 [H]
+ * Limits: b <= 2^22, 8 <= H <= 32768, H % 8 == 0, group 0 or 128.
+ */
+int moe_tail_norm_quant(const void* x, const void* residual, const void* gamma, float gain_center,
+                        float eps, int b, int H, int q_dtype, int group, void* residual_out, void* y,
+                        void* q, void* scale, void* stream);
+
+/*
+ * v = silu(gate) * up in 8 bits, FP32 until the rounding; silu(g) = g / (1 + exp(-g)).
+ *   gate_up    BF16 [rows][2 I]: a row's I gate columns, then its I up columns
+ *   used_rows  device int32, or NULL: only rows below it are read and written
+ *              (expert_offsets + num_experts, where routes have been dropped)
+ *   q          [rows][I]
+ * Limits: rows <= 2^22, 8 <= I <= 32768, I % 8 == 0, group 0 or 128.
+ */
+int moe_tail_silu_quant(const void* gate_up, const int32_t* used_rows, int rows, int I, int q_dtype,
+                        int group, void* q, void* scale, void* stream);
+
+/*
+ * Routes sorted by expert.  Route r = t * K + k goes to expert_ids[t][k]; an
+ * id outside [0, num_experts) has no place (an expert of another device).
+ *   expert_offsets[e]   int32 [num_experts + 1]: routes with a smaller id, so
+ *                       expert e's rows are [expert_offsets[e], expert_offsets[e + 1])
+ *   permuted_idx[t][k]  int32 [b][K]: the route's row, or -1.  Rows of one
+ *                       expert are in route order.
+ *   source[row]         int32 [b * K]: the row's route, -1 past the last row
+ *   workspace           >= moe_tail_sort_workspace_bytes(b, K, num_experts)
+ *                       bytes, 16-byte aligned
+ * b = 0 writes expert_offsets (zeros) and nothing else.
+ * Limits: 1 <= K <= 32, b * K <= 2^21, num_experts <= 1024.
+ */
+int moe_tail_sort_routes(const int32_t* expert_ids, int b, int K, int num_experts,
+                         int32_t* expert_offsets, int32_t* permuted_idx, int32_t* source,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t moe_tail_sort_workspace_bytes(int b, int K, int num_experts);
+
+/*
+ * rows[permuted_idx[t][k]] = x[t] for every route whose index is in [0, num_rows),
+ * and row_scale likewise from scale [b] (both NULL where rows have no scale).
+ * Rows that no route names are not written.  No two routes name one row
+ * (moe_tail_sort_routes' index).
+ *   x [b][H], rows [num_rows][H] of elem_bytes (1 or 2) bytes an element
+ * The gradient of x is moe_tail_combine_rows of the rows' gradients with
+ * route_weights NULL.
+ * Limits: 1 <= K <= 32, b * K <= 2^22, num_rows <= 2^22, 8 <= H <= 32768, H % 8 == 0.
+ */
+int moe_tail_dispatch_rows(const void* x, const void* scale, const int32_t* permuted_idx, int b,
+                           int K, int H, int elem_bytes, int64_t num_rows, void* rows,
+                           void* row_scale, void* stream);
+
+/*
+ * The weighted sum back to tokens, without a norm (the finalize calls have one):
+ *   out[t] = bf16( sum over k in order of w[t][k] * fp32(rows[permuted_idx[t][k]]) )
+ * FP32 from +0 over the routes whose index is in [0, num_rows); the others are
+ * skipped, whatever their weight.  A token without a row gets zeros.
+ *   rows BF16 [num_rows][H], route_weights [b][K] FP32 or BF16, or NULL: ones
+ *   out  BF16 [b][H]
+ * Limits: as moe_tail_dispatch_rows.
+ */
+int moe_tail_combine_rows(const void* rows, int64_t num_rows, const int32_t* permuted_idx,
+                          const void* route_weights, int weight_dtype, int b, int K, int H, void* out,
+                          void* stream);
+
+/*
+ * The gradients of that sum, given d_out (BF16 [b][H]):
+ *   d_rows[permuted_idx[t][k]] = bf16( w[t][k] * fp32(d_out[t]) )    BF16 [num_rows][H]
+ *   d_weights[t][k] = sum( fp32(d_out[t]) * fp32(rows[permuted_idx[t][k]]) )   FP32 [b][K]
+ * A route without a row has d_weights 0; rows that no route names are not
+ * written.  No two routes name one row.  Limits: as moe_tail_dispatch_rows.
+ */
+int moe_tail_combine_grad(const void* d_out, const void* rows, int64_t num_rows,
+                          const int32_t* permuted_idx, const void* route_weights, int weight_dtype,
+                          int b, int K, int H, void* d_rows, void* d_weights, void* stream);
+
+/*
+ * 8-bit integer product with a scale for each row and each channel, by expert:
+ *   out[r][n] = bf16( (sum over k of x[r][k] * w[e][n][k]) * w_scale[e][n] * x_scale[r] )
+ * for the rows r of [expert_offsets[e], expert_offsets[e + 1]).  Rows of no
+ * expert are not written.
+ *   x         int8 [rows][D]          x_scale  FP32 [rows]
+ *   w         int8 [num_experts][N][D]  w_scale  FP32 [num_experts][N]
+ *   expert_offsets  device int32 [num_experts + 1], ascending within [0, rows]
+ *                   (moe_tail_sort_routes), or NULL: one expert has every row
+ *   out       BF16 [rows][N]
+ *   workspace >= moe_tail_expert_product_workspace_bytes(rows, num_experts, N, D)
+ *             bytes, 256-byte aligned
+ * Limits: rows <= 2^22, num_experts <= 1024, 8 <= N <= 2^20, N % 8 == 0,
+ * 16 <= D <= 65536, D % 16 == 0.
+ */
+int moe_tail_expert_product(const void* x, const void* x_scale, const void* w, const void* w_scale,
+                            const int32_t* expert_offsets, int64_t rows, int num_experts, int N, int D,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t moe_tail_expert_product_workspace_bytes(int64_t rows, int num_experts, int N, int D);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,12 +22,16 @@ __all__ = [
     "moe_shared_gate_up", "moe_shared_down", "moe_tail_latent_up_flags", "moe_tail_ep_finalize_flags",
     "moe_tail_tp_finalize_flags", "moe_tail_set_kernel_form", "kernel_form", "FORM_EP", "FORM_TP", "FORM_LATENT",
     "FORM_LATENT_ONE_KERNEL", "moe_tail_set_stage_wait_limit", "moe_tail_up_project_shared_down",
-    "moe_shared_down_persistent",
+    "moe_shared_down_persistent", "moe_tail_norm_quant", "moe_tail_silu_quant", "moe_tail_sort_routes",
+    "moe_tail_sort_workspace_bytes", "moe_tail_dispatch_rows", "moe_tail_combine_rows", "moe_tail_combine_grad",
+    "moe_tail_expert_product", "moe_tail_expert_product_workspace_bytes",
 ]
 
 OK, EINVAL, ECUDA, ENOTSUP = 0, 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 1 << 20  # MOE_TAIL_NOALLOC_SCRATCH_BYTES
 W_FP32, W_BF16 = 0, 1
+Q_DTYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}  # MOE_TAIL_Q_*: the types of 8-bit rows
+QUANT_GROUP = 128  # columns of a group where a row has several scales
 WEIGHTS_STATIC = 1  # MOE_TAIL_WEIGHTS_STATIC
 INPUTS_READY = 2  # MOE_TAIL_INPUTS_READY
 FORM_EP, FORM_TP, FORM_LATENT = 0, 1, 2  # MOE_TAIL_FORM_*: the calls whose kernel form can be pinned
@@ -78,7 +82,20 @@ def lib() -> ctypes.CDLL:
         L.moe_tail_set_kernel_form.argtypes = [i32, i32]
         L.moe_tail_set_stage_wait_limit.argtypes = [ctypes.c_ulonglong]
         L.moe_tail_up_project_shared_down.argtypes = [P, P, P, i32, P, P, i32, i32, i32, i32, P, P, i32, P]
+        L.moe_tail_norm_quant.argtypes = [P, P, P, f32, f32, i32, i32, i32, i32, P, P, P, P, P]
+        L.moe_tail_silu_quant.argtypes = [P, P, i32, i32, i32, i32, P, P, P]
+        L.moe_tail_sort_routes.argtypes = [P, i32, i32, i32, P, P, P, P, sz, P]
+        L.moe_tail_sort_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_tail_sort_workspace_bytes.restype = sz
+        L.moe_tail_dispatch_rows.argtypes = [P, P, P, i32, i32, i32, i32, i64, P, P, P]
+        L.moe_tail_combine_rows.argtypes = [P, i64, P, P, i32, i32, i32, i32, P, P]
+        L.moe_tail_combine_grad.argtypes = [P, P, i64, P, P, i32, i32, i32, i32, P, P, P]
+        L.moe_tail_expert_product.argtypes = [P, P, P, P, P, i64, i32, i32, i32, P, P, sz, P]
+        L.moe_tail_expert_product_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.moe_tail_expert_product_workspace_bytes.restype = sz
         for name in ("moe_tail_ep_finalize", "moe_tail_tp_finalize", "moe_tail_latent_up", "moe_shared_expert",
+                     "moe_tail_norm_quant", "moe_tail_silu_quant", "moe_tail_sort_routes", "moe_tail_dispatch_rows",
+                     "moe_tail_combine_rows", "moe_tail_combine_grad", "moe_tail_expert_product",
                      "moe_tail_take_device_error", "moe_tail_latent_up_noalloc", "moe_tail_selftest_wait_timeout",
                      "moe_tail_latent_norm", "moe_tail_up_project", "moe_shared_gate_up", "moe_shared_down",
                      "moe_tail_latent_up_flags", "moe_tail_ep_finalize_flags", "moe_tail_tp_finalize_flags",
@@ -395,6 +412,170 @@ def moe_shared_expert(x, w_gate, w_up, w_down, out, workspace, *, accumulate=Tru
     _cuda(x, w_gate, w_up, w_down, out, workspace)
     _check("moe_shared_expert", lib().moe_shared_expert(
         _p(x), _p(w_gate), _p(w_up), _p(w_down), b, H, I, _p(out), int(bool(accumulate)), _p(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def _eight_bits(q, scale, rows: int, width: int, group: int) -> int:
+    """The type code of 8-bit rows q [rows, width] and their FP32 scales: [rows]
+    (group 0) or [rows, ceil(width / 128)] (group 128)."""
+    if q.dtype not in Q_DTYPES:
+        raise ValueError(f"q must be torch.int8 or torch.float8_e4m3fn, got {q.dtype}")
+    if group not in (0, QUANT_GROUP):
+        raise ValueError(f"group must be 0 (one scale a row) or {QUANT_GROUP}, got {group}")
+    _like("q", q, q.dtype, (rows, width))
+    _like("scale", scale, torch.float32, (rows, -(-width // group)) if group else (rows,))
+    return Q_DTYPES[q.dtype]
+
+
+def moe_tail_norm_quant(x, residual, gamma, q, scale, *, residual_out=None, y=None, gain_center=1.0, eps=1e-6, group=0,
+                        stream=None):
+    """h = x + residual, its RMS norm with gains gamma + gain_center, in 8 bits
+    into q (int8 or float8_e4m3fn [b, H]) and scale (FP32 [b], or with
+    group=128 [b, ceil(H / 128)]); x, residual BF16 [b, H] (residual may be
+    None), gamma BF16 [H].  residual_out (BF16 [b, H], may be x or residual)
+    receives bf16(h), y the normed row in BF16.  Returns (q, scale)."""
+    b, H = _dims("x", x, 2)
+    _like("x", x, torch.bfloat16, (b, H))
+    _like("gamma", gamma, torch.bfloat16, (H,))
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+        if t is not None:
+            _like(name, t, torch.bfloat16, (b, H))
+    kind = _eight_bits(q, scale, b, H, group)
+    _cuda(x, residual, gamma, q, scale, residual_out, y)
+    _check("moe_tail_norm_quant", lib().moe_tail_norm_quant(
+        _p(x), _p(residual), _p(gamma), gain_center, eps, b, H, kind, group, _p(residual_out), _p(y), _p(q), _p(scale),
+        _stream(stream)))
+    return q, scale
+
+
+def moe_tail_silu_quant(gate_up, q, scale, *, used_rows=None, group=0, stream=None):
+    """silu(gate) * up in 8 bits into q (int8 or float8_e4m3fn [rows, I]) and
+    scale (as for moe_tail_norm_quant); gate_up BF16 [rows, 2 I], a row's gate
+    columns before its up columns.  used_rows (int32 CUDA tensor of one
+    element): rows from it on are neither read nor written.  Returns (q, scale)."""
+    rows, I2 = _dims("gate_up", gate_up, 2)
+    _like("gate_up", gate_up, torch.bfloat16, (rows, I2 // 2 * 2))
+    if used_rows is not None:
+        if used_rows.numel() != 1:
+            raise ValueError(f"used_rows must have one element, got shape {tuple(used_rows.shape)}")
+        _like("used_rows", used_rows, torch.int32, used_rows.shape)
+    kind = _eight_bits(q, scale, rows, I2 // 2, group)
+    _cuda(gate_up, q, scale, used_rows)
+    _check("moe_tail_silu_quant", lib().moe_tail_silu_quant(
+        _p(gate_up), _p(used_rows), rows, I2 // 2, kind, group, _p(q), _p(scale), _stream(stream)))
+    return q, scale
+
+
+def moe_tail_sort_workspace_bytes(b: int, K: int, num_experts: int) -> int:
+    return int(lib().moe_tail_sort_workspace_bytes(b, K, num_experts))
+
+
+def moe_tail_sort_routes(expert_ids, expert_offsets, permuted_idx, source, workspace, *, stream=None):
+    """The routes of expert_ids (int32 [b, K]) sorted by expert, stably:
+    expert_offsets (int32 [num_experts + 1]), permuted_idx (int32 [b, K], a
+    route's row or -1 where its id is outside [0, num_experts)) and source
+    (int32 [b * K], a row's route or -1).  workspace: a CUDA tensor of at least
+    moe_tail_sort_workspace_bytes(b, K, num_experts) bytes."""
+    b, K = _dims("expert_ids", expert_ids, 2)
+    E = _dims("expert_offsets", expert_offsets, 1)[0] - 1
+    _like("expert_ids", expert_ids, torch.int32, (b, K))
+    _like("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _like("permuted_idx", permuted_idx, torch.int32, (b, K))
+    _like("source", source, torch.int32, (b * K,))
+    _cuda(expert_ids, expert_offsets, permuted_idx, source, workspace)
+    _check("moe_tail_sort_routes", lib().moe_tail_sort_routes(
+        _p(expert_ids), b, K, E, _p(expert_offsets), _p(permuted_idx), _p(source), _p(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return expert_offsets, permuted_idx, source
+
+
+def moe_tail_dispatch_rows(x, permuted_idx, rows, *, scale=None, row_scale=None, stream=None) -> torch.Tensor:
+    """rows[permuted_idx[t, k]] = x[t]: x [b, H] and rows [num_rows, H] of one
+    type (BF16, int8 or float8_e4m3fn), permuted_idx int32 [b, K]; 8-bit rows'
+    scales likewise from scale (FP32 [b]) into row_scale (FP32 [num_rows])."""
+    b, H = _dims("x", x, 2)
+    num_rows, _ = _dims("rows", rows, 2)
+    _, K = _dims("permuted_idx", permuted_idx, 2)
+    if x.dtype != torch.bfloat16 and x.dtype not in Q_DTYPES:
+        raise ValueError(f"x must be torch.bfloat16, torch.int8 or torch.float8_e4m3fn, got {x.dtype}")
+    _like("rows", rows, x.dtype, (num_rows, H))
+    _like("permuted_idx", permuted_idx, torch.int32, (b, K))
+    if (scale is None) != (row_scale is None):
+        raise ValueError("scale and row_scale must be given together")
+    if scale is not None:
+        _like("scale", scale, torch.float32, (b,))
+        _like("row_scale", row_scale, torch.float32, (num_rows,))
+    _cuda(x, permuted_idx, rows, scale, row_scale)
+    _check("moe_tail_dispatch_rows", lib().moe_tail_dispatch_rows(
+        _p(x), _p(scale), _p(permuted_idx), b, K, H, x.element_size(), num_rows, _p(rows), _p(row_scale),
+        _stream(stream)))
+    return rows
+
+
+def moe_tail_combine_rows(rows, permuted_idx, route_weights, out, *, stream=None) -> torch.Tensor:
+    """out[t] (BF16 [b, H]) = the sum over t's routes, in order, of their weight
+    times their row of rows (BF16 [num_rows, H]); permuted_idx int32 [b, K],
+    route_weights FP32 or BF16 [b, K], or None for ones (the gradient of
+    moe_tail_dispatch_rows, given the rows' gradients)."""
+    num_rows, H = _dims("rows", rows, 2)
+    b, K = _dims("permuted_idx", permuted_idx, 2)
+    _like("rows", rows, torch.bfloat16, (num_rows, H))
+    _like("permuted_idx", permuted_idx, torch.int32, (b, K))
+    if route_weights is not None:
+        _weights(route_weights)
+        _like("route_weights", route_weights, route_weights.dtype, (b, K))
+    _like("out", out, torch.bfloat16, (b, H))
+    _cuda(rows, permuted_idx, route_weights, out)
+    _check("moe_tail_combine_rows", lib().moe_tail_combine_rows(
+        _p(rows), num_rows, _p(permuted_idx), _p(route_weights),
+        W_FP32 if route_weights is None else _weights(route_weights), b, K, H, _p(out), _stream(stream)))
+    return out
+
+
+def moe_tail_combine_grad(d_out, rows, permuted_idx, route_weights, d_rows, d_weights, *, stream=None):
+    """The gradients of moe_tail_combine_rows given d_out (BF16 [b, H]): d_rows
+    (BF16 [num_rows, H]) and d_weights (FP32 [b, K], whatever the weights'
+    type).  Returns (d_rows, d_weights)."""
+    b, H = _dims("d_out", d_out, 2)
+    num_rows, _ = _dims("rows", rows, 2)
+    _, K = _dims("permuted_idx", permuted_idx, 2)
+    _like("d_out", d_out, torch.bfloat16, (b, H))
+    _like("rows", rows, torch.bfloat16, (num_rows, H))
+    _like("permuted_idx", permuted_idx, torch.int32, (b, K))
+    wdtype = _weights(route_weights)
+    _like("route_weights", route_weights, route_weights.dtype, (b, K))
+    _like("d_rows", d_rows, torch.bfloat16, (num_rows, H))
+    _like("d_weights", d_weights, torch.float32, (b, K))
+    _cuda(d_out, rows, permuted_idx, route_weights, d_rows, d_weights)
+    _check("moe_tail_combine_grad", lib().moe_tail_combine_grad(
+        _p(d_out), _p(rows), num_rows, _p(permuted_idx), _p(route_weights), wdtype, b, K, H, _p(d_rows), _p(d_weights),
+        _stream(stream)))
+    return d_rows, d_weights
+
+
+def moe_tail_expert_product_workspace_bytes(rows: int, num_experts: int, N: int, D: int) -> int:
+    return int(lib().moe_tail_expert_product_workspace_bytes(rows, num_experts, N, D))
+
+
+def moe_tail_expert_product(x, x_scale, w, w_scale, out, workspace, *, expert_offsets=None, stream=None) -> torch.Tensor:
+    """out (BF16 [rows, N]) = x (int8 [rows, D], x_scale FP32 [rows]) times the
+    transpose of each row's expert's weight w[e] (int8 [num_experts, N, D],
+    w_scale FP32 [num_experts, N]); expert_offsets int32 [num_experts + 1]
+    (moe_tail_sort_routes), or None with one expert.  workspace: a CUDA tensor
+    of at least moe_tail_expert_product_workspace_bytes(rows, num_experts, N, D) bytes."""
+    rows, D = _dims("x", x, 2)
+    E, N, _ = _dims("w", w, 3)
+    _like("x", x, torch.int8, (rows, D))
+    _like("x_scale", x_scale, torch.float32, (rows,))
+    _like("w", w, torch.int8, (E, N, D))
+    _like("w_scale", w_scale, torch.float32, (E, N))
+    if expert_offsets is not None:
+        _like("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _like("out", out, torch.bfloat16, (rows, N))
+    _cuda(x, x_scale, w, w_scale, expert_offsets, out, workspace)
+    _check("moe_tail_expert_product", lib().moe_tail_expert_product(
+        _p(x), _p(x_scale), _p(w), _p(w_scale), _p(expert_offsets), rows, E, N, D, _p(out), _p(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 

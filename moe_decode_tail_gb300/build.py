@@ -20,7 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoetail.so")
 TRACE_LIB = os.path.join(BUILD, "libmoetail_trace.so")  # the same kernels with the per-CTA trace
 FLOOR_LIB = os.path.join(BUILD, "libmoetail_floor.so")  # latency-floor kernels (measurement only)
-SOURCES = ["finalize.cu", "decode_gemm.cu", "moe_tail_api.cu", "noalloc.cu"]
+SOURCES = ["finalize.cu", "decode_gemm.cu", "moe_tail_api.cu", "noalloc.cu", "row_quant.cu", "routes.cu", "expert_product.cu",
+           "layer_api.cu"]
 FLOOR_SOURCES = ["floor.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

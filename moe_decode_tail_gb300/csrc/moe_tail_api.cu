@@ -15,9 +15,8 @@
 #include <utility>
 
 #include "../../include/moe_tail.h"
+#include "host_util.h"
 #include "kernels.h"
-
-#define MOE_API extern "C" __attribute__((visibility("default")))
 
 // ============================================================================ host-side configuration
 
@@ -126,40 +125,6 @@ using moetail::kMaxTokens;
 using moetail::kMaxTp;
 using moetail::kMaxWidth;
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-Range span(const void* p, size_t bytes) { return Range{(uintptr_t)p, (uintptr_t)p + bytes}; }
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-int finish(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_TAIL_OK;
-  (void)cudaGetLastError();
-  return MOE_TAIL_ECUDA;
-}
-
-// ---- TMA descriptors --------------------------------------------------------
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static EncodeTiled fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiled>(p);
-  });
-  return fn;
-}
-
 // Row-major BF16 matrix [rows][cols] read in boxes of box_rows x 64 columns
 // (128 bytes: the swizzle span), 128-byte swizzle; out-of-range boxes read zeros.
 bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
@@ -174,8 +139,6 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t co
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promo,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 int check_finalize_common(const void* w, int weight_dtype, const void* gamma, int b, int tp, int K, int P,
                           void* out) {

@@ -1,0 +1,269 @@
+// Routes sorted by expert, rows copied into that order and back with weights, and the gradients (sm_103a).
+//
+//   sort      a stable counting sort of the routes r = t * K + k by expert id
+//   dispatch  rows[idx[t][k]] = x[t]
+//   combine   out[t] = bf16(sum over k, in order, of w[t][k] * rows[idx[t][k]])      (FP32 from +0)
+//   gradient  d_rows[idx[t][k]] = bf16(w[t][k] * d_out[t]),  d_w[t][k] = sum(d_out[t] * rows[idx[t][k]])
+//
+// A route has a row iff 0 <= idx < num_rows; a route without one is skipped, whatever its weight.
+#include "common.cuh"
+#include "kernels.h"
+#include "layer.h"
+
+namespace moetail {
+
+namespace {
+
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortPerLane = kSortChunk / kSortThreads;
+
+// Routes of each expert in every chunk of kSortChunk routes.
+__global__ void __launch_bounds__(kSortThreads) count_routes_kernel(const SortArgs a) {
+  extern __shared__ int32_t s_count[];
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) s_count[e] = 0;
+  grid_dependency_wait();
+  launch_dependents();
+  __syncthreads();
+  const int r0 = blockIdx.x * kSortChunk;
+#pragma unroll
+  for (int j = 0; j < kSortPerLane; ++j) {
+    const int r = r0 + j * kSortThreads + threadIdx.x;
+    const int e = r < a.routes ? a.ids[r] : -1;
+    if (e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);  // whole numbers: the order does not matter
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kSortThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = s_count[e];
+}
+
+// Exclusive sum over the 1024 threads; *all: the total.
+__device__ __forceinline__ int block_exclusive_sum(int v, int* all) {
+  __shared__ int s_warp[kSortWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sum = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += o;
+  }
+  if (lane == 31) s_warp[warp] = sum;
+  __syncthreads();
+  int w = s_warp[lane];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, w, off);
+    if (lane >= off) w += o;
+  }
+  *all = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  __syncthreads();
+  return sum - v + (warp > 0 ? before : 0);
+}
+
+// Places of a chunk's routes.  A warp takes 32 * kSortPerLane consecutive routes, 32 at a time, so the order
+// within an expert is: earlier chunks, earlier warps, earlier rounds, lower lanes.
+__global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortArgs a) {
+  extern __shared__ int32_t s_mem[];  // [warps][E] counts, then the routes of the warps before; [E] first place
+  int32_t* s_first = s_mem + kSortWarps * a.E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) s_mem[i] = 0;
+  grid_dependency_wait();
+  launch_dependents();
+  __syncthreads();
+  const int r0 = blockIdx.x * kSortChunk + warp * 32 * kSortPerLane + lane;
+  int32_t* mine = s_mem + warp * a.E;
+  int id[kSortPerLane], rank[kSortPerLane];
+#pragma unroll
+  for (int j = 0; j < kSortPerLane; ++j) {
+    const int r = r0 + 32 * j;
+    id[j] = r < a.routes ? a.ids[r] : -1;
+    if (id[j] >= a.E) id[j] = -1;
+  }
+#pragma unroll
+  for (int j = 0; j < kSortPerLane; ++j) {
+    const unsigned same = __match_any_sync(0xffffffffu, id[j] < 0 ? -1 : id[j]);
+    const unsigned below = same & ((1u << lane) - 1u);
+    rank[j] = 0;
+    if (id[j] >= 0) rank[j] = mine[id[j]] + __popc(below);
+    __syncwarp();
+    if (id[j] >= 0 && below == 0) mine[id[j]] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  const int e = threadIdx.x;  // E <= 1024
+  int total = 0, before = 0;
+  if (e < a.E) {
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = s_mem[w * a.E + e];
+      s_mem[w * a.E + e] = total;
+      total += n;
+    }
+    if (gridDim.x > 1) {
+      total = 0;
+      for (int c = 0; c < (int)gridDim.x; ++c) {
+        const int n = a.counts[(int64_t)c * a.E + e];
+        if (c < (int)blockIdx.x) before += n;
+        total += n;
+      }
+    }
+  }
+  int all;
+  const int first = block_exclusive_sum(total, &all);
+  if (e < a.E) {
+    s_first[e] = first + before;
+    if (blockIdx.x == 0) a.offsets[e] = first;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kSortPerLane; ++j) {
+    const int r = r0 + 32 * j;
+    if (r >= a.routes) continue;
+    int place = -1;
+    if (id[j] >= 0) {
+      place = s_first[id[j]] + mine[id[j]] + rank[j];
+      a.source[place] = r;
+    }
+    a.permuted_idx[r] = place;
+    if (r >= all) a.source[r] = -1;  // places past the last row
+  }
+}
+
+// ---- rows ---------------------------------------------------------------------------
+
+// V: 16 or 8 bytes.  A thread copies one vector of a token's row to the places of all its routes.
+template <typename V>
+__global__ void __launch_bounds__(256) dispatch_rows_kernel(const DispatchArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int t = blockIdx.x;
+  const int nv = a.row_bytes / (int)sizeof(V);
+  const V* src = reinterpret_cast<const V*>(a.x) + (int64_t)t * nv;
+  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
+    const V d = src[v];
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t j = a.idx[(int64_t)t * a.K + k];
+      if (j >= 0 && j < a.num_rows) reinterpret_cast<V*>(a.rows)[j * nv + v] = d;
+    }
+  }
+  if (a.scale && blockIdx.y == 0 && threadIdx.x < a.K) {
+    const int64_t j = a.idx[(int64_t)t * a.K + threadIdx.x];
+    if (j >= 0 && j < a.num_rows) a.row_scale[j] = a.scale[t];
+  }
+}
+
+template <int WMODE>
+__device__ __forceinline__ float route_weight(const void* w, int64_t i) {
+  if (WMODE == kWeightUnit) return 1.0f;
+  if (WMODE == kWeightBF16) return bf16_lo(static_cast<const uint16_t*>(w)[i]);
+  return static_cast<const float*>(w)[i];
+}
+
+template <int WMODE>
+__global__ void __launch_bounds__(256) combine_rows_kernel(const CombineArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int nv = a.H >> 3;
+  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t j = a.idx[t * a.K + k];
+      if (j < 0 || j >= a.num_rows) continue;
+      const float w = route_weight<WMODE>(a.w, t * a.K + k);
+      float f[8];
+      unpack8(ld_stream_v4(a.rows + j * a.H + 8 * v), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += w * f[e];
+    }
+    st_v4(a.out + t * a.H + 8 * v, make_uint4(pack_bf16x2_pz(acc[0], acc[1]), pack_bf16x2_pz(acc[2], acc[3]),
+                                              pack_bf16x2_pz(acc[4], acc[5]), pack_bf16x2_pz(acc[6], acc[7])));
+  }
+}
+
+// A block per token: d_out's row stays in registers while the routes' rows pass.
+template <int WMODE, int VPT>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineArgs a) {
+  __shared__ float s_dot[kMaxK][32];
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int nv = a.H >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint4 d[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nv) d[i] = ld_stream_v4(a.d_out + t * a.H + 8 * v);
+  }
+  for (int k = 0; k < a.K; ++k) {
+    const int64_t j = a.idx[t * a.K + k];
+    const bool live = j >= 0 && j < a.num_rows;
+    float dot = 0.0f;
+    if (live) {
+      const float w = route_weight<WMODE>(a.w, t * a.K + k);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v >= nv) continue;
+        float f[8], g[8];
+        unpack8(ld_stream_v4(a.rows + j * a.H + 8 * v), f);
+        unpack8(d[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += f[e] * g[e];
+        st_v4(a.d_rows + j * a.H + 8 * v,
+              make_uint4(pack_bf16x2_pz(w * g[0], w * g[1]), pack_bf16x2_pz(w * g[2], w * g[3]),
+                         pack_bf16x2_pz(w * g[4], w * g[5]), pack_bf16x2_pz(w * g[6], w * g[7])));
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (lane == 0) s_dot[k][warp] = dot;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < a.K) {
+    float dot = 0.0f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) dot += s_dot[threadIdx.x][w];
+    a.d_w[t * a.K + threadIdx.x] = dot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t stream) {
+  const int blocks = a.routes > kSortChunk ? (a.routes + kSortChunk - 1) / kSortChunk : 1;
+  const size_t smem = (size_t)(kSortWarps + 1) * a.E * 4;
+  cudaError_t e = ensure_smem_limit((const void*)place_routes_kernel, (kSortWarps + 1) * kMaxExperts * 4);
+  if (e != cudaSuccess) return e;
+  if (blocks > 1) {
+    e = launch_pdl(count_routes_kernel, dim3(blocks), dim3(kSortThreads), (size_t)a.E * 4, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(place_routes_kernel, dim3(blocks), dim3(kSortThreads), smem, stream, a);
+}
+
+cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t stream) {
+  const bool wide = a.row_bytes % 16 == 0;
+  const int nv = a.row_bytes / (wide ? 16 : 8);
+  const dim3 grid(a.b, (nv + 255) / 256);
+  if (wide) return launch_pdl(dispatch_rows_kernel<uint4>, grid, dim3(256), 0, stream, a);
+  return launch_pdl(dispatch_rows_kernel<uint2>, grid, dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
+  const int nv = a.H >> 3;
+  const dim3 grid(a.b, (nv + 255) / 256);
+  if (wmode == kWeightUnit) return launch_pdl(combine_rows_kernel<kWeightUnit>, grid, dim3(256), 0, stream, a);
+  if (wmode == kWeightBF16) return launch_pdl(combine_rows_kernel<kWeightBF16>, grid, dim3(256), 0, stream, a);
+  return launch_pdl(combine_rows_kernel<kWeightF32>, grid, dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
+  const int nv = a.H >> 3;
+  const int threads = ((nv + 3) / 4 + 31) / 32 * 32;
+  if (wmode == kWeightBF16)
+    return launch_pdl(combine_grad_kernel<kWeightBF16, 4>, dim3(a.b), dim3(threads), 0, stream, a);
+  return launch_pdl(combine_grad_kernel<kWeightF32, 4>, dim3(a.b), dim3(threads), 0, stream, a);
+}
+
+}  // namespace moetail

@@ -1,0 +1,259 @@
+// Rows in 8 bits with scales: residual addition + RMS norm, and silu(gate) * up (sm_103a).
+//
+//   norm_quant   h = x + residual (FP32); residual_out = bf16(h);
+//                y = (h * inv) * (gamma + gain_center), inv = 1 / sqrt(sum(h^2) * (1/H) + eps)
+//   silu_quant   y = (gate / (1 + exp(-gate))) * up
+//   both         per group (a whole row, or 128 columns): scale = max|y| / M, q = round(y * (M / max|y|)),
+//                M = 127 (int8) or 448 (e4m3), to nearest even; a group of zeros has scale 0 and zeros,
+//                a group with a NaN or an infinity scale NaN and zeros.
+//
+// A thread block per row, 16-byte loads of 8 columns; the values stay in registers between the reduction and
+// the rounding, so every input is read once.  Bound by memory: 4 + 2 + 1 bytes a column for the norm, 4 + 1
+// for silu.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "layer.h"
+
+namespace moetail {
+
+namespace {
+
+// |v| as ordered bits: infinities are above every finite value and NaNs above them, so one unsigned maximum
+// finds the largest magnitude and whether anything was not finite.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// What a group's largest magnitude gives: its scale, and the factors of the rounding.  Below 2^-100, M / top
+// could overflow, so the values are lifted by 2^100 first (exact); elsewhere that factor is 1.
+struct Rounding {
+  float scale, lift, factor;
+  __device__ Rounding(uint32_t top_bits, float most) {
+    const float top = __uint_as_float(top_bits);
+    lift = top < 0x1p-100f ? 0x1p100f : 1.0f;
+    factor = top_bits == 0 ? 0.0f : most / (top * lift);
+    scale = top / most;
+    if (top_bits >= 0x7f800000u) {
+      scale = __uint_as_float(0x7fffffffu);
+      factor = 0.0f;
+    }
+  }
+};
+
+// Eight values rounded to 8 bits.  A group that is not finite (scale NaN) gives zeros.
+template <int KIND>
+__device__ __forceinline__ uint2 round8(const float (&y)[8], const Rounding& r) {
+  const bool fine = r.scale == r.scale;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fine ? (y[i] * r.lift) * r.factor : 0.0f;
+  uint2 q;
+  if (KIND == kQuantInt8) {
+    auto pack4 = [](float a, float b, float c, float d) {
+      // |v| is at most 127 (1 + 2^-22): it rounds to at most 127
+      uint32_t hi, all;
+      asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(__float2int_rn(d)), "r"(__float2int_rn(c)));
+      asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
+          : "=r"(all)
+          : "r"(__float2int_rn(b)), "r"(__float2int_rn(a)), "r"(hi));
+      return all;
+    };
+    q.x = pack4(v[0], v[1], v[2], v[3]);
+    q.y = pack4(v[4], v[5], v[6], v[7]);
+  } else {
+    auto pair = [](float lo, float hi) {
+      return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    };
+    q.x = pair(v[0], v[1]) | (pair(v[2], v[3]) << 16);
+    q.y = pair(v[4], v[5]) | (pair(v[6], v[7]) << 16);
+  }
+  return q;
+}
+
+constexpr float most_of(int kind) { return kind == kQuantInt8 ? 127.0f : 448.0f; }
+
+__device__ __forceinline__ uint32_t max8(const float (&y)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude(y[i]));
+  return m;
+}
+
+// The maximum over the 16 lanes of a 128-column group.
+__device__ __forceinline__ uint32_t max_of_group(uint32_t m) {
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+
+// Sum and maximum over the thread block, in a fixed order, known to every thread.
+struct RowSums {
+  float sum;
+  uint32_t top;
+};
+__device__ __forceinline__ RowSums block_reduce(float sum, uint32_t top) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_top[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (warps > 1) {
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_top[warp] = top;
+    }
+    __syncthreads();
+    sum = lane < warps ? s_sum[lane] : 0.0f;
+    top = lane < warps ? s_top[lane] : 0u;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  return RowSums{sum, top};
+}
+
+// VPT: vectors of 8 columns of a thread; thread t holds vectors t, t + blockDim, ...
+template <int KIND, bool GROUPED, int VPT>
+__global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t row = blockIdx.x;
+  const int nv = a.H >> 3;
+  float h[VPT][8];
+  float sum = 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nv) {
+      const int64_t at = row * a.H + 8 * v;
+      unpack8(*reinterpret_cast<const uint4*>(a.x + at), h[i]);
+      if (a.residual) {
+        float r[8];
+        unpack8(*reinterpret_cast<const uint4*>(a.residual + at), r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += h[i][e] * h[i][e];
+  }
+  float inv = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {  // h * gain, kept apart from h until the row's norm is known
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nv && a.residual_out) {
+      const int64_t at = row * a.H + 8 * v;
+      st_v4(a.residual_out + at, make_uint4(pack_bf16x2_pz(h[i][0], h[i][1]), pack_bf16x2_pz(h[i][2], h[i][3]),
+                                            pack_bf16x2_pz(h[i][4], h[i][5]), pack_bf16x2_pz(h[i][6], h[i][7])));
+    }
+  }
+  const RowSums first = block_reduce(sum, 0u);
+  inv = __fdiv_rn(1.0f, __fsqrt_rn(first.sum * a.rcpH + a.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nv) {
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.gamma + 8 * v), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * inv) * (g[e] + a.gain_center);
+      if (a.y)
+        st_v4(a.y + row * a.H + 8 * v, make_uint4(pack_bf16x2_pz(h[i][0], h[i][1]), pack_bf16x2_pz(h[i][2], h[i][3]),
+                                                  pack_bf16x2_pz(h[i][4], h[i][5]), pack_bf16x2_pz(h[i][6], h[i][7])));
+    }
+    top = max(top, max8(h[i]));
+  }
+  if (!GROUPED) {
+    __syncthreads();  // the first reduction's shared values have been read
+    top = block_reduce(0.0f, top).top;
+    if (threadIdx.x == 0) a.scale[row] = Rounding(top, most_of(KIND)).scale;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    const Rounding r(GROUPED ? max_of_group(max8(h[i])) : top, most_of(KIND));
+    if (v < nv) {
+      *reinterpret_cast<uint2*>(a.q + row * a.H + 8 * v) = round8<KIND>(h[i], r);
+      if (GROUPED && (v & 15) == 0) a.scale[row * a.groups + (v >> 4)] = r.scale;
+    }
+  }
+}
+
+template <int KIND, bool GROUPED, int VPT>
+__global__ void __launch_bounds__(1024) silu_quant_kernel(const SiluQuantArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t row = blockIdx.x;
+  if (a.used && row >= *a.used) return;
+  const int nv = a.I >> 3;
+  float y[VPT][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nv) {
+      const uint16_t* src = a.gate_up + row * 2 * a.I + 8 * v;
+      float u[8];
+      unpack8(*reinterpret_cast<const uint4*>(src), y[i]);
+      unpack8(*reinterpret_cast<const uint4*>(src + a.I), u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] / (1.0f + expf(-y[i][e])) * u[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[i][e] = 0.0f;
+    }
+    top = max(top, max8(y[i]));
+  }
+  if (!GROUPED) {
+    top = block_reduce(0.0f, top).top;
+    if (threadIdx.x == 0) a.scale[row] = Rounding(top, most_of(KIND)).scale;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    const Rounding r(GROUPED ? max_of_group(max8(y[i])) : top, most_of(KIND));
+    if (v < nv) {
+      *reinterpret_cast<uint2*>(a.q + row * a.I + 8 * v) = round8<KIND>(y[i], r);
+      if (GROUPED && (v & 15) == 0) a.scale[row * a.groups + (v >> 4)] = r.scale;
+    }
+  }
+}
+
+// A row's vectors over the threads of a block: VPT vectors each, whole warps.
+int threads_for(int nv, int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; }
+
+}  // namespace
+
+cudaError_t launch_norm_quant(const NormQuantArgs& a, int kind, bool grouped, int sms, cudaStream_t stream) {
+  const int nv = a.H >> 3;
+  auto launch = [&](auto kernel, int vpt) {
+    return launch_pdl(kernel, dim3(a.b), dim3(threads_for(nv, vpt)), 0, stream, a);
+  };
+#define MOE_PICK(VPT)                                                                                        \
+  (kind == kQuantInt8 ? (grouped ? launch(norm_quant_kernel<kQuantInt8, true, VPT>, VPT)                     \
+                                 : launch(norm_quant_kernel<kQuantInt8, false, VPT>, VPT))                   \
+                      : (grouped ? launch(norm_quant_kernel<kQuantE4M3, true, VPT>, VPT)                     \
+                                 : launch(norm_quant_kernel<kQuantE4M3, false, VPT>, VPT)))
+  return nv <= 1024 ? MOE_PICK(1) : MOE_PICK(4);
+#undef MOE_PICK
+}
+
+cudaError_t launch_silu_quant(const SiluQuantArgs& a, int kind, bool grouped, int sms, cudaStream_t stream) {
+  const int nv = a.I >> 3;
+  auto launch = [&](auto kernel, int vpt) {
+    return launch_pdl(kernel, dim3((unsigned)a.rows), dim3(threads_for(nv, vpt)), 0, stream, a);
+  };
+#define MOE_PICK(VPT)                                                                                        \
+  (kind == kQuantInt8 ? (grouped ? launch(silu_quant_kernel<kQuantInt8, true, VPT>, VPT)                     \
+                                 : launch(silu_quant_kernel<kQuantInt8, false, VPT>, VPT))                   \
+                      : (grouped ? launch(silu_quant_kernel<kQuantE4M3, true, VPT>, VPT)                     \
+                                 : launch(silu_quant_kernel<kQuantE4M3, false, VPT>, VPT)))
+  return nv <= 1024 ? MOE_PICK(1) : MOE_PICK(4);
+#undef MOE_PICK
+}
+
+}  // namespace moetail
