@@ -88,14 +88,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // Barrier 1 over the four epilogue warps only.
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Byte offset, in a K-major operand tile of 128-byte rows written with the
-// 128-byte swizzle, of the 16-byte unit u (columns 8u..8u+7) of row r: the
-// unit index is XORed with the row's position in its 8-row group, as a TMA
-// box lands with CU_TENSOR_MAP_SWIZZLE_128B (tile bases 1024-aligned).
-__device__ __forceinline__ uint32_t sw128_offset(int r, int u) {
-  return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4));
-}
-
 // Cluster rank whose K range holds K block kb under the even split of
 // kblocks over ksplit ranks (the first kb_rem ranks take one more).
 __device__ __forceinline__ uint32_t kblock_owner(int kb, int kb_per, int kb_rem) {

@@ -2,102 +2,584 @@
 //
 //   out[r][n] = bf16((sum over k of x[r][k] * w[e][n][k]) * w_scale[e][n] * x_scale[r]),
 //   r in [offsets[e], offsets[e + 1])
+//
+// sm_103a's tensor cores have no fast 8-bit integer form, but every int8 is an FP16 number and a product of two
+// is exact in FP32, so the product runs as kind::f16: exact while the magnitudes add up to less than 2^24, and
+// rounded to FP32 beyond.  The weights cross memory once, as bytes, and become FP16 on the way to the tensor core:
+//
+//   expand   (own kernel) the rows x in FP16 into the workspace: small beside the weights, and every channel
+//            tile reads them again
+//   product  persistent, one thread block an SM.  A tile is 128 channels of an expert (the MMA's M) by up to NT
+//            of its rows (its N).  The weight bytes arrive by TMA (128 channels x 128 bytes a stage); eight warps
+//            turn them into FP16 in registers and store them into tensor memory, from where the MMA takes its A
+//            operand (a thread's row is a TMEM lane, so nothing is shuffled or written back to shared memory);
+//            the FP16 rows arrive by TMA as the B operand; four warps read finished accumulators, scale them and
+//            write BF16.  Warp roles meet at mbarriers only, so the weight stream runs on across tiles.
+//
+// Where the tiles are too few for the SMs, each is split along the reduction; a part's FP32 sums go to the
+// workspace and the block that finishes a tile's last part adds them, in the order of the parts.
+//
+// Every wait is bounded in time; on expiry the kernel raises a bit in the device error word, lets its copies and
+// MMAs finish, frees its tensor memory and returns.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
+#include "kernels.h"
 #include "layer.h"
+#include "tensor_core.cuh"
 
 namespace moetail {
 
 namespace {
 
+__device__ unsigned int g_product_error = 0;
+__device__ __forceinline__ void raise_error(unsigned bit) { atomicOr(&g_product_error, bit); }
+
+constexpr int kTileM = 128;                    // channels of a tile
+constexpr int kWBlock = 128;                   // reduction bytes of a weight stage: one swizzle row
+constexpr int kWStage = kTileM * kWBlock;      // 16 KB
+constexpr int kXBlock = 64;                    // FP16 of a row stage: one swizzle row
+constexpr int kAColumns = kXBlock / 2;         // TMEM columns of a weight half stage: two FP16 each
+constexpr int kEpilogueWarps = 4, kConvertWarps = 8;
+constexpr int kWarpW = kEpilogueWarps + kConvertWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
+constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kMaxParts = 320;                 // parts (tiles x splits) with FP32 sums in the workspace
+constexpr int kMaxSplit = 8;
+
+struct Args {
+  const float* x_scale;
+  const float* w_scale;
+  const int32_t* offsets;
+  uint16_t* out;
+  float* partial;      // [kMaxParts][NT][128]
+  unsigned* counters;  // [kMaxParts]: finished parts of a tile, zeroed by the expand kernel
+  int64_t R;
+  int E, N;
+  int w_blocks;        // ceil(D / 128)
+  int w_stages, x_stages;
+  unsigned long long stage_wait_ns;
+};
+
 // Offsets come from the device: whatever they hold, no row outside [0, R) is touched.
 __device__ __forceinline__ int clamp_row(int r, int64_t rows) { return r < 0 ? 0 : r > rows ? (int)rows : r; }
 
-constexpr int kTileN = 64, kTileR = 32, kTileD = 64;
+// ---- int8 to FP16 -----------------------------------------------------------------
 
-__global__ void __launch_bounds__(256) expert_product_kernel(const ProductArgs a) {
-  __shared__ int s_w[kTileN][kTileD / 4 + 1], s_x[kTileR][kTileD / 4 + 1];
-  __shared__ int s_tile[2];
+// Four int8 as two pairs of FP16.  The byte v + 128 under the exponent of 1024 is the FP16 number 1152 + v, and
+// the subtraction is exact.
+__device__ __forceinline__ void int8x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = v ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 base = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), base);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), base);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint16_t* x16, const int32_t* offsets, int E,
+                                                          int64_t R, int D, unsigned* counters) {
   grid_dependency_wait();
+  // Only now: when the product's blocks start, everything before this call is complete, so they may read the
+  // weights, scales and offsets at once and wait for this kernel before they touch what it writes.
   launch_dependents();
-  // the block's tile: row tiles are counted expert by expert
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < kMaxParts; i += blockDim.x) counters[i] = 0;
+  const int64_t rows = offsets ? clamp_row(offsets[E], R) : R;
+  const int64_t n = rows * D / 16;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(x + 16 * i);
+    uint4 a, b;
+    int8x4_to_f16(v.x, a.x, a.y);
+    int8x4_to_f16(v.y, a.z, a.w);
+    int8x4_to_f16(v.z, b.x, b.y);
+    int8x4_to_f16(v.w, b.z, b.w);
+    st_v4(x16 + 16 * i, a);
+    st_v4(x16 + 16 * i + 8, b);
+  }
+}
+
+// ---- PTX of this kernel -------------------------------------------------------------
+
+// D[tmem_d] (+)= A[tmem_a] * B[bdesc], FP16 operands, FP32 sums.
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f16 with FP16 operands: FP32 accumulate (bits 4-5 = 1), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
+__device__ __forceinline__ uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// 32 consecutive TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// Barrier 1 over the four epilogue warps; whether `ok` holds in all of them.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+// mbar_wait by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs, abort_flag));
+}
+
+// ---- the product ----------------------------------------------------------------------
+
+// A part: reduction blocks [k0, k0 + blocks) of 128 channels from m0 by rows [r0, r0 + rows) of expert e.
+struct Part {
+  int e, m0, r0, rows, k0, blocks, tile;
+  bool shared;  // more than one row tile reads this expert's weights
+};
+
+// NT: rows of a tile (the accumulator's columns).
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                          const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr int kXStage = NT * kXBlock * 2;
+  constexpr int kBox = NT < 64 ? NT : 64;          // rows of one TMA box
+  constexpr int kAccs = NT > 128 ? 1 : 2;          // accumulators, taken in turn
+  constexpr int kAStages = 8;                      // weight half stages in tensor memory
+  constexpr uint32_t kTmemA = kAccs * NT;          // first column of the A ring
+  static_assert(kTmemA + kAStages * kAColumns <= 512, "tensor memory");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  const uint32_t w_ring = base, x_ring = w_ring + (uint32_t)(a.w_stages * kWStage);
+  uint32_t at = x_ring + (uint32_t)(a.x_stages * kXStage);
+  auto bars = [&](int n) {
+    const uint32_t first = at;
+    at += 8u * n;
+    return first;
+  };
+  const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages);
+  const uint32_t x_full = bars(a.x_stages), x_empty = bars(a.x_stages);
+  const uint32_t a_full = bars(kAStages), a_empty = bars(kAStages);
+  const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
+  volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort, last part
+  volatile uint32_t* abort_ptr = word + 1;
+  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16);  // [E + 1] row tiles before an expert
+  int32_t* s_row = s_first + a.E + 1;                                          // [E] an expert's first row
+  int32_t* s_count = s_row + a.E;                                              // [E] its rows
+
   if (threadIdx.x == 0) {
-    int left = blockIdx.x, e = -1, first = 0;
-    if (!a.offsets) {
-      e = 0;
-      first = left * kTileR;
-    } else {
-      for (int i = 0; i < a.E; ++i) {
-        const int begin = clamp_row(a.offsets[i], a.R), end = clamp_row(a.offsets[i + 1], a.R);
-        const int tiles = end > begin ? (end - begin + kTileR - 1) / kTileR : 0;
-        if (left < tiles) {
-          e = i;
-          first = begin + left * kTileR;
-          break;
-        }
-        left -= tiles;
-      }
+    for (int s = 0; s < a.w_stages; ++s) {
+      mbar_init(w_full + 8 * s, 1);
+      mbar_init(w_empty + 8 * s, kConvertWarps);
     }
-    s_tile[0] = e;
-    s_tile[1] = first;
+    for (int s = 0; s < a.x_stages; ++s) {
+      mbar_init(x_full + 8 * s, 1);
+      mbar_init(x_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < kAStages; ++s) {
+      mbar_init(a_full + 8 * s, kConvertWarps / 2);
+      mbar_init(a_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < kAccs; ++s) {
+      mbar_init(acc_full + 8 * s, 1);
+      mbar_init(acc_empty + 8 * s, kEpilogueWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_ptr = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
+  }
+  if (warp == kWarpMma) tmem_alloc(at, 512);
+  // The experts' rows and row tiles.  The offsets were complete before the expand kernel let this one start.
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    const int begin = a.offsets ? clamp_row(a.offsets[e], a.R) : 0;
+    const int end = a.offsets ? clamp_row(a.offsets[e + 1], a.R) : (int)a.R;
+    s_row[e] = begin;
+    s_count[e] = end > begin ? end - begin : 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  launch_dependents();
+  const uint32_t tmem = word[0];
+  if (warp == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int tiles = e < a.E ? (s_count[e] + NT - 1) / NT : 0;
+      int sum = tiles;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      if (e < a.E) s_first[e] = before + sum - tiles;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) s_first[a.E] = before;
   }
   __syncthreads();
-  const int e = s_tile[0];
-  if (e < 0) return;
-  const int64_t first = s_tile[1], end = a.offsets ? clamp_row(a.offsets[e + 1], a.R) : a.R;
-  const int n0 = blockIdx.y * kTileN;
-  const int tn = threadIdx.x & 31, tr = threadIdx.x >> 5;  // 2 channels x 4 rows a thread
-  int acc[4][2] = {};
-  for (int k0 = 0; k0 < a.D; k0 += kTileD) {
-    for (int i = threadIdx.x; i < (kTileN + kTileR) * (kTileD / 16); i += 256) {
-      const int row = i / (kTileD / 16), c = i % (kTileD / 16), k = k0 + 16 * c;
-      int4 v = make_int4(0, 0, 0, 0);
-      if (row < kTileN) {
-        if (n0 + row < a.N && k < a.D)
-          v = *reinterpret_cast<const int4*>(a.w + ((int64_t)e * a.N + n0 + row) * a.D + k);
-      } else if (first + row - kTileN < end && k < a.D) {
-        v = *reinterpret_cast<const int4*>(a.x + (first + row - kTileN) * a.D + k);
-      }
-      int* dst = row < kTileN ? &s_w[row][4 * c] : &s_x[row - kTileN][4 * c];
-      dst[0] = v.x;
-      dst[1] = v.y;
-      dst[2] = v.z;
-      dst[3] = v.w;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kTileD / 4; ++c) {
-      const int w0 = s_w[tn][c], w1 = s_w[tn + 32][c];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = s_x[tr + 8 * i][c];
-        acc[i][0] = __dp4a(w0, x, acc[i][0]);
-        acc[i][1] = __dp4a(w1, x, acc[i][1]);
+
+  const int m_tiles = (a.N + kTileM - 1) / kTileM;
+  const int64_t tiles = (int64_t)s_first[a.E] * m_tiles;
+  // Parts of a tile: the split with the least work in a row for a block, a part's fixed cost counted as two
+  // reduction blocks.
+  int split = 1;
+  {
+    int64_t least = (tiles + gridDim.x - 1) / gridDim.x * (a.w_blocks + 2);
+    for (int s = 2; s <= kMaxSplit && s <= a.w_blocks && tiles * s <= kMaxParts; ++s) {
+      const int64_t cost = (tiles * s + gridDim.x - 1) / gridDim.x * ((a.w_blocks + s - 1) / s + 2);
+      if (cost < least) {
+        least = cost;
+        split = s;
       }
     }
-    __syncthreads();
   }
+  const int64_t parts = tiles * split;
+  // Parts in the order (expert, channel tile, row tile, split): neighbours share a weight tile.
+  auto part_of = [&](int64_t p) {
+    Part q;
+    const int64_t tile = p / split;
+    const int s = (int)(p - tile * split);
+    int lo = 0, hi = a.E - 1;  // the last expert whose tiles start at or before this one
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)s_first[mid] * m_tiles <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const int row_tiles = s_first[lo + 1] - s_first[lo];
+    const int left = (int)(tile - (int64_t)s_first[lo] * m_tiles);
+    const int m = left / row_tiles, t = left - m * row_tiles;
+    q.e = lo;
+    q.m0 = m * kTileM;
+    q.r0 = s_row[lo] + t * NT;
+    q.rows = min(NT, s_count[lo] - t * NT);
+    q.k0 = (int)((int64_t)s * a.w_blocks / split);
+    q.blocks = (int)((int64_t)(s + 1) * a.w_blocks / split) - q.k0;
+    q.tile = (int)(split > 1 ? tile : 0);
+    q.shared = row_tiles > 1;
+    return q;
+  };
+  auto give_up = [&](unsigned bit) {
+    if (!*abort_ptr) raise_error(bit);
+    *abort_ptr = 1;
+  };
+
+  if (warp == kWarpW) {
+    // ---------------- weight bytes ----------------
+    if (lane == 0) {
+      const uint64_t once = policy_evict_first(), again = policy_evict_last();
+      int g = 0;
+      bool ok = true;
+      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
+        const Part q = part_of(p);
+        for (int i = 0; i < q.blocks; ++i, ++g) {
+          const int s = g % a.w_stages;
+          if (g >= a.w_stages &&
+              !mbar_wait(w_empty + 8 * s, (uint32_t)(g / a.w_stages - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+            give_up(kErrWaitEmpty);
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(w_full + 8 * s, kWStage);
+          tma_load_3d(w_ring + s * kWStage, &map_w, w_full + 8 * s, (q.k0 + i) * kWBlock, q.m0, q.e,
+                      q.shared ? again : once);
+        }
+      }
+      for (int i = max(0, g - a.w_stages); i < g; ++i)  // copies in flight land before the block's memory goes away
+        if (!mbar_wait(w_full + 8 * (i % a.w_stages), (uint32_t)(i / a.w_stages) & 1u)) raise_error(kErrWaitDrain);
+    }
+    __syncwarp();
+  } else if (warp == kWarpX) {
+    // ---------------- FP16 rows ----------------
+    if (lane == 0) {
+      grid_dependency_wait();  // the expand kernel's rows
+      const uint64_t keep = policy_evict_last();
+      int g = 0;
+      bool ok = true;
+      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
+        const Part q = part_of(p);
+        const int boxes = (q.rows + kBox - 1) / kBox;
+        for (int i = 0; i < 2 * q.blocks; ++i, ++g) {
+          const int s = g % a.x_stages;
+          if (g >= a.x_stages &&
+              !mbar_wait(x_empty + 8 * s, (uint32_t)(g / a.x_stages - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+            give_up(kErrWaitEmpty);
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(x_full + 8 * s, (uint32_t)(boxes * kBox * kXBlock * 2));
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(x_ring + s * kXStage + b * kBox * kXBlock * 2, &map_x, x_full + 8 * s,
+                        (2 * q.k0 + i) * kXBlock, q.r0 + b * kBox, keep);
+        }
+      }
+      for (int i = max(0, g - a.x_stages); i < g; ++i)
+        if (!mbar_wait(x_full + 8 * (i % a.x_stages), (uint32_t)(i / a.x_stages) & 1u)) raise_error(kErrWaitDrain);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
+      int g = 0, done = 0;
+      bool ok = true;
+      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, ++done) {
+        const Part q = part_of(p);
+        const int buf = done % kAccs;
+        if (done >= kAccs &&
+            !mbar_wait(acc_empty + 8 * buf, (uint32_t)(done / kAccs - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+          give_up(kErrWaitAccum);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t idesc = idesc_f16(kTileM, (q.rows + 15) & ~15);
+        for (int i = 0; i < 2 * q.blocks; ++i, ++g) {
+          const int sx = g % a.x_stages, sa = g % kAStages;
+          if (!mbar_wait(x_full + 8 * sx, (uint32_t)(g / a.x_stages) & 1u, limit, abort_ptr) ||
+              !mbar_wait(a_full + 8 * sa, (uint32_t)(g / kAStages) & 1u, kWaitLimitNs, abort_ptr)) {
+            give_up(kErrWaitFull);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t bdesc = smem_desc_sw128(x_ring + sx * kXStage);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = first + tr + 8 * i;
-    if (r >= end) continue;
+          for (int kk = 0; kk < kXBlock / 16; ++kk)  // 16 FP16: 8 columns of A, 32 bytes along B's swizzled row
+            mma_f16_ts(tmem + buf * NT, tmem + kTmemA + sa * kAColumns + 8 * kk, bdesc + 2 * kk, idesc,
+                       (i > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(a_empty + 8 * sa);
+          mma_commit(x_empty + 8 * sx);
+        }
+        if (ok) mma_commit(acc_full + 8 * buf);
+      }
+      mma_commit(mma_done);  // the MMAs that were issued are done before tensor memory is freed
+      if (!mbar_wait(mma_done, 0)) raise_error(kErrWaitAccum);
+    }
+    __syncwarp();
+  } else if (warp >= kEpilogueWarps) {
+    // ---------------- int8 to FP16: half stage `half` of every weight stage, one TMEM lane a thread ----------------
+    const int half = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    int g = 0;  // weight stages
+    bool ok = true;
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
+      const Part q = part_of(p);
+      for (int i = 0; i < q.blocks; ++i, ++g) {
+        const int s = g % a.w_stages, g2 = 2 * g + half, sa = g2 % kAStages;
+        if (!warp_wait(w_full + 8 * s, (uint32_t)(g / a.w_stages) & 1u, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
+          break;
+        }
+        const uint32_t st = w_ring + s * kWStage;
+        uint32_t r[32];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = n0 + tn + 32 * j;
-      if (n < a.N)
-        a.out[r * a.N + n] =
-            (uint16_t)bf16_bits_pz((float)acc[i][j] * a.w_scale[(int64_t)e * a.N + n] * a.x_scale[r]);
+        for (int u = 0; u < 4; ++u) {
+          const uint4 v = ld_shared_v4(st + sw128_offset(row, 4 * half + u));
+          int8x4_to_f16(v.x, r[8 * u], r[8 * u + 1]);
+          int8x4_to_f16(v.y, r[8 * u + 2], r[8 * u + 3]);
+          int8x4_to_f16(v.z, r[8 * u + 4], r[8 * u + 5]);
+          int8x4_to_f16(v.w, r[8 * u + 6], r[8 * u + 7]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w_empty + 8 * s);
+        if (g2 >= kAStages && !warp_wait(a_empty + 8 * sa, (uint32_t)(g2 / kAStages - 1) & 1u, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitEmpty);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32(tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + sa * kAColumns, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_full + 8 * sa);
+      }
+    }
+  } else {
+    // ---------------- accumulators to BF16 ----------------
+    grid_dependency_wait();  // the counters
+    int done = 0;
+    bool ok = true;
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, ++done) {
+      const Part q = part_of(p);
+      const int buf = done % kAccs;
+      const int n = q.m0 + warp * 32 + lane;
+      const float ws = n < a.N ? a.w_scale[(int64_t)q.e * a.N + n] : 0.0f;
+      ok = warp_wait(acc_full + 8 * buf, (uint32_t)(done / kAccs) & 1u, abort_ptr);
+      if (split > 1) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
+      if (!ok) {
+        if (lane == 0) give_up(kErrWaitAccum);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(warp * 32) << 16) + buf * NT;
+      float* mine = split > 1 ? a.partial + (int64_t)p * NT * kTileM + warp * 32 + lane : nullptr;
+      auto finish16 = [&](const float (&v)[16], int c) {
+        const int r = c + (lane & 15);
+        const float xs = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float s = __shfl_sync(0xffffffffu, xs, i);
+          if (c + i < q.rows && n < a.N)
+            a.out[(int64_t)(q.r0 + c + i) * a.N + n] = (uint16_t)bf16_bits_pz(v[i] * ws * s);
+        }
+      };
+#pragma unroll 1
+      for (int c = 0; c < q.rows; c += 16) {
+        float v[16];
+        tmem_ld16(src + c, v);
+        if (split == 1) {
+          finish16(v, c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(c + i) * kTileM] = v[i];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+      if (split > 1) {
+        __threadfence();
+        epilogue_all(true);
+        if (threadIdx.x == 0) word[2] = atomicAdd(&a.counters[q.tile], 1u);
+        epilogue_all(true);
+        if (word[2] == (unsigned)(split - 1)) {  // the tile's last part: add them all, in order
+          __threadfence();
+          const float* first = a.partial + (int64_t)q.tile * split * NT * kTileM + warp * 32 + lane;
+#pragma unroll 1
+          for (int c = 0; c < q.rows; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            for (int s = 0; s < split; ++s) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += __ldcg(first + ((int64_t)s * NT + c + i) * kTileM);
+            }
+            finish16(v, c);
+          }
+        }
+        epilogue_all(true);  // before word[2] is written again
+      }
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+// Rows of a tile: all of them where one expert has few, else twice an expert's average share, so that an uneven
+// batch still has one row tile for most experts.
+int rows_of_tile(int64_t R, int E) {
+  const int64_t want = E == 1 ? R : 2 * ((R + E - 1) / E);
+  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+}
+
+size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+struct Layout {  // of the workspace, from its 256-aligned start
+  size_t x16, counters, partial, bytes;
+};
+Layout layout(int64_t R, int E, int D) {
+  Layout l;
+  l.x16 = 0;
+  l.counters = round_up((size_t)R * D * 2, 256);
+  l.partial = l.counters + round_up(kMaxParts * 4, 256);
+  l.bytes = l.partial + (size_t)kMaxParts * kTileM * rows_of_tile(R, E) * 4;
+  return l;
+}
+
+template <int NT>
+cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
+  constexpr int kLimit = 227 * 1024;
+  constexpr int kXStage = NT * kXBlock * 2;
+  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (4 * 16 + 2 * 8 + 5);
+  a.x_stages = NT >= 256 ? 4 : 8;
+  a.w_stages = (kLimit - fixed - a.x_stages * kXStage) / kWStage;
+  if (a.w_stages > 12) a.w_stages = 12;
+  auto kernel = expert_product_kernel<NT>;
+  cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
+  if (e != cudaSuccess) return e;
+  const size_t smem = fixed + (size_t)a.x_stages * kXStage + (size_t)a.w_stages * kWStage;
+  return launch_pdl(kernel, dim3(sms), dim3(kThreads), smem, stream, map_w, map_x, a);
 }
 
 }  // namespace
 
-size_t expert_product_workspace(int64_t, int, int, int) { return 256; }
+size_t expert_product_workspace(int64_t R, int E, int, int D) { return layout(R, E, D).bytes; }
 
-cudaError_t launch_expert_product(const ProductArgs& a, void*, int, cudaStream_t stream) {
-  // row tiles: the full ones, and at most one more for every expert with a row
-  const int64_t tiles = a.R / kTileR + (a.offsets ? (a.E < a.R ? a.E : a.R) : 1);
-  return launch_pdl(expert_product_kernel, dim3((unsigned)tiles, (a.N + kTileN - 1) / kTileN), dim3(256), 0, stream, a);
+int product_rows_of_tile(int64_t R, int E) { return rows_of_tile(R, E); }
+
+cudaError_t launch_expert_product(const ProductArgs& p, const CUtensorMap& map_w, const CUtensorMap& map_x,
+                                  void* workspace, int sms, cudaStream_t stream) {
+  const Layout l = layout(p.R, p.E, p.D);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Args a;
+  a.x_scale = p.x_scale;
+  a.w_scale = p.w_scale;
+  a.offsets = p.offsets;
+  a.out = p.out;
+  a.partial = reinterpret_cast<float*>(ws + l.partial);
+  a.counters = reinterpret_cast<unsigned*>(ws + l.counters);
+  a.R = p.R;
+  a.E = p.E;
+  a.N = p.N;
+  a.w_blocks = (p.D + kWBlock - 1) / kWBlock;
+  a.stage_wait_ns = stage_wait_limit_ns();
+  const int64_t vectors = p.R * p.D / 16;
+  const int64_t blocks = (vectors + 255) / 256;
+  cudaError_t e = launch_pdl(expand_rows_kernel, dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, stream,
+                             p.x, reinterpret_cast<uint16_t*>(ws + l.x16), p.offsets, p.E, p.R, p.D, a.counters);
+  if (e != cudaSuccess) return e;
+  switch (rows_of_tile(p.R, p.E)) {
+    case 16: return launch_nt<16>(map_w, map_x, a, sms, stream);
+    case 32: return launch_nt<32>(map_w, map_x, a, sms, stream);
+    case 64: return launch_nt<64>(map_w, map_x, a, sms, stream);
+    case 128: return launch_nt<128>(map_w, map_x, a, sms, stream);
+    default: return launch_nt<256>(map_w, map_x, a, sms, stream);
+  }
+}
+
+cudaError_t take_product_error(unsigned* bits) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_product_error, sizeof v);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_product_error, &zero, sizeof zero);
+  *bits = v;
+  return e;
 }
 
 }  // namespace moetail

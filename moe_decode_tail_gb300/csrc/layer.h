@@ -110,7 +110,13 @@ struct ProductArgs {
   int E, N, D;
   uint16_t* out;           // BF16 [R][N]
 };
-cudaError_t launch_expert_product(const ProductArgs& a, void* workspace, int sms, cudaStream_t stream);
+// map_w: w as [E][N][D] bytes, boxes of 128 channels x 128 bytes; map_x: the FP16 rows at the workspace's start,
+// [R][D], boxes of min(product_rows_of_tile, 64) rows x 64; both with the 128-byte swizzle, zeros out of range.
+cudaError_t launch_expert_product(const ProductArgs& a, const CUtensorMap& map_w, const CUtensorMap& map_x,
+                                  void* workspace, int sms, cudaStream_t stream);
 size_t expert_product_workspace(int64_t R, int E, int N, int D);
+int product_rows_of_tile(int64_t R, int E);
+// Read and clear the product's device error word (synchronises).
+cudaError_t take_product_error(unsigned* bits);
 
 }  // namespace moetail

@@ -227,6 +227,26 @@ MOE_API int moe_tail_combine_grad(const void* d_out, const void* rows, int64_t n
 
 namespace {
 
+// int8 [E][N][D] read in boxes of 128 channels x 128 bytes, and FP16 [R][D] in boxes of box_rows x 64 (128 bytes
+// each: the swizzle span); out-of-range parts of a box read zeros.
+bool encode_product_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const void* x16, int64_t R, int E, int N,
+                         int D, int box_rows) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t wd[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)E};
+  const cuuint64_t wst[2] = {(cuuint64_t)D, (cuuint64_t)D * N};
+  const cuuint32_t wb[3] = {128, 128, 1}, ones[3] = {1, 1, 1};
+  const cuuint64_t xd[2] = {(cuuint64_t)D, (cuuint64_t)R};
+  const cuuint64_t xst[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t xb[2] = {64, (cuuint32_t)box_rows};
+  return enc(map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w), wd, wst, wb, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         enc(map_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(x16), xd, xst, xb, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool product_sizes_ok(int64_t R, int E, int N, int D) {
   return R >= 0 && R <= kMaxRows && E >= 1 && E <= kMaxExperts && N >= 8 && N <= kMaxN && N % 8 == 0 && D >= 16 &&
          D <= kMaxD && D % 16 == 0;
@@ -264,5 +284,10 @@ MOE_API int moe_tail_expert_product(const void* x, const void* x_scale, const vo
   a.N = N;
   a.D = D;
   a.out = static_cast<uint16_t*>(out);
-  return finish(moetail::launch_expert_product(a, workspace, device_sms(), static_cast<cudaStream_t>(stream)));
+  const int tile = moetail::product_rows_of_tile(rows, num_experts);
+  CUtensorMap map_w, map_x;
+  if (!encode_product_maps(&map_w, &map_x, w, workspace, rows, num_experts, N, D, tile < 64 ? tile : 64))
+    return MOE_TAIL_ECUDA;
+  return finish(
+      moetail::launch_expert_product(a, map_w, map_x, workspace, device_sms(), static_cast<cudaStream_t>(stream)));
 }

@@ -17,6 +17,7 @@
 #include "../../include/moe_tail.h"
 #include "host_util.h"
 #include "kernels.h"
+#include "layer.h"
 
 // ============================================================================ host-side configuration
 
@@ -615,10 +616,11 @@ MOE_API const char* moe_tail_status_str(int status) {
 
 MOE_API int moe_tail_take_device_error(unsigned int* bits) {
   if (!bits) return MOE_TAIL_EINVAL;
-  unsigned g = 0, f = 0;
+  unsigned g = 0, f = 0, p = 0;
   cudaError_t e = moetail::take_device_error(&g);
   if (e == cudaSuccess) e = moetail::take_finalize_error(&f);
-  *bits = g | f;
+  if (e == cudaSuccess) e = moetail::take_product_error(&p);
+  *bits = g | f | p;
   return finish(e);
 }
 

@@ -129,4 +129,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// Byte offset, in a K-major operand tile of 128-byte rows written with the
+// 128-byte swizzle, of the 16-byte unit u (columns 8u..8u+7) of row r: the
+// unit index is XORed with the row's position in its 8-row group, as a TMA
+// box lands with CU_TENSOR_MAP_SWIZZLE_128B (tile bases 1024-aligned).
+__device__ __forceinline__ uint32_t sw128_offset(int r, int u) {
+  return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4));
+}
+
 }  // namespace moetail
