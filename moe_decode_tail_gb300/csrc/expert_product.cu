@@ -150,10 +150,32 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
       : "memory");
   return all != 0;
 }
-// mbar_wait by a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs, abort_flag));
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                         unsigned long long limit_ns = kWaitLimitNs) {
+  return mbar_wait(bar, parity, limit_ns, abort_flag);
 }
+// By a whole warp: its first lane asks (32 lanes asking at once are served one by one), the others get its answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, abort_flag);
+  ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+  __syncwarp();
+  return ok;
+}
+
+// A place in a ring of `stages` slots and the parity of its current round (counted, not divided: an integer
+// division a step was most of the MMA thread's time).
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;  // of the round: a consumer waits for it on "full", a producer for its opposite on "empty"
+  __device__ __forceinline__ void step(int stages, int by = 1) {
+    slot += by;
+    if (slot >= stages) {
+      slot -= stages;
+      parity ^= 1u;
+    }
+  }
+};
 
 // ---- the product ----------------------------------------------------------------------
 
@@ -300,24 +322,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- weight bytes ----------------
     if (lane == 0) {
       const uint64_t once = policy_evict_first(), again = policy_evict_last();
-      int g = 0;
+      int64_t g = 0;
+      Ring w;
       bool ok = true;
       for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
         const Part q = part_of(p);
-        for (int i = 0; i < q.blocks; ++i, ++g) {
-          const int s = g % a.w_stages;
-          if (g >= a.w_stages &&
-              !mbar_wait(w_empty + 8 * s, (uint32_t)(g / a.w_stages - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+        for (int i = 0; i < q.blocks; ++i, ++g, w.step(a.w_stages)) {
+          if (!wait_for(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
             give_up(kErrWaitEmpty);
             ok = false;
             break;
           }
-          mbar_expect_tx(w_full + 8 * s, kWStage);
-          tma_load_3d(w_ring + s * kWStage, &map_w, w_full + 8 * s, (q.k0 + i) * kWBlock, q.m0, q.e,
+          mbar_expect_tx(w_full + 8 * w.slot, kWStage);
+          tma_load_3d(w_ring + w.slot * kWStage, &map_w, w_full + 8 * w.slot, (q.k0 + i) * kWBlock, q.m0, q.e,
                       q.shared ? again : once);
         }
       }
-      for (int i = max(0, g - a.w_stages); i < g; ++i)  // copies in flight land before the block's memory goes away
+      for (int64_t i = g > a.w_stages ? g - a.w_stages : 0; i < g; ++i)  // copies in flight land before the block's memory goes away
         if (!mbar_wait(w_full + 8 * (i % a.w_stages), (uint32_t)(i / a.w_stages) & 1u)) raise_error(kErrWaitDrain);
     }
     __syncwarp();
@@ -326,15 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       grid_dependency_wait();  // the expand kernel's rows
       const uint64_t keep = policy_evict_last();
-      int g = 0;
+      int64_t g = 0;
+      Ring x;
       bool ok = true;
       for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
         const Part q = part_of(p);
         const int boxes = (q.rows + kBox - 1) / kBox;
-        for (int i = 0; i < 2 * q.blocks; ++i, ++g) {
-          const int s = g % a.x_stages;
-          if (g >= a.x_stages &&
-              !mbar_wait(x_empty + 8 * s, (uint32_t)(g / a.x_stages - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+        for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(a.x_stages)) {
+          const int s = x.slot;
+          if (!wait_for(x_empty + 8 * s, x.parity ^ 1u, abort_ptr)) {
             give_up(kErrWaitEmpty);
             ok = false;
             break;
@@ -345,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (2 * q.k0 + i) * kXBlock, q.r0 + b * kBox, keep);
         }
       }
-      for (int i = max(0, g - a.x_stages); i < g; ++i)
+      for (int64_t i = g > a.x_stages ? g - a.x_stages : 0; i < g; ++i)
         if (!mbar_wait(x_full + 8 * (i % a.x_stages), (uint32_t)(i / a.x_stages) & 1u)) raise_error(kErrWaitDrain);
     }
     __syncwarp();
@@ -353,22 +374,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
-      int g = 0, done = 0;
+      Ring x, w, acc;
       bool ok = true;
-      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, ++done) {
+      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
         const Part q = part_of(p);
-        const int buf = done % kAccs;
-        if (done >= kAccs &&
-            !mbar_wait(acc_empty + 8 * buf, (uint32_t)(done / kAccs - 1) & 1u, kWaitLimitNs, abort_ptr)) {
+        const int buf = acc.slot;
+        if (!wait_for(acc_empty + 8 * buf, acc.parity ^ 1u, abort_ptr)) {
           give_up(kErrWaitAccum);
           break;
         }
         tc_fence_after();
         const uint32_t idesc = idesc_f16(kTileM, (q.rows + 15) & ~15);
-        for (int i = 0; i < 2 * q.blocks; ++i, ++g) {
-          const int sx = g % a.x_stages, sa = g % kAStages;
-          if (!mbar_wait(x_full + 8 * sx, (uint32_t)(g / a.x_stages) & 1u, limit, abort_ptr) ||
-              !mbar_wait(a_full + 8 * sa, (uint32_t)(g / kAStages) & 1u, kWaitLimitNs, abort_ptr)) {
+        for (int i = 0; i < 2 * q.blocks; ++i, x.step(a.x_stages), w.step(kAStages)) {
+          const int sx = x.slot, sa = w.slot;
+          if (!wait_for(x_full + 8 * sx, x.parity, abort_ptr, limit) ||
+              !wait_for(a_full + 8 * sa, w.parity, abort_ptr)) {
             give_up(kErrWaitFull);
             ok = false;
             break;
@@ -392,13 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- int8 to FP16: half stage `half` of every weight stage, one TMEM lane a thread ----------------
     const int half = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    int g = 0;  // weight stages
+    Ring w, half_stage;
+    half_stage.slot = half;
     bool ok = true;
     for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
       const Part q = part_of(p);
-      for (int i = 0; i < q.blocks; ++i, ++g) {
-        const int s = g % a.w_stages, g2 = 2 * g + half, sa = g2 % kAStages;
-        if (!warp_wait(w_full + 8 * s, (uint32_t)(g / a.w_stages) & 1u, abort_ptr)) {
+      for (int i = 0; i < q.blocks; ++i, w.step(a.w_stages), half_stage.step(kAStages, 2)) {
+        const int s = w.slot, sa = half_stage.slot;
+        if (!warp_wait(w_full + 8 * s, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
           break;
@@ -415,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(w_empty + 8 * s);
-        if (g2 >= kAStages && !warp_wait(a_empty + 8 * sa, (uint32_t)(g2 / kAStages - 1) & 1u, abort_ptr)) {
+        if (!warp_wait(a_empty + 8 * sa, half_stage.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
           break;
@@ -430,14 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- accumulators to BF16 ----------------
     grid_dependency_wait();  // the counters
-    int done = 0;
+    Ring acc;
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, ++done) {
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
       const Part q = part_of(p);
-      const int buf = done % kAccs;
+      const int buf = acc.slot;
       const int n = q.m0 + warp * 32 + lane;
       const float ws = n < a.N ? a.w_scale[(int64_t)q.e * a.N + n] : 0.0f;
-      ok = warp_wait(acc_full + 8 * buf, (uint32_t)(done / kAccs) & 1u, abort_ptr);
+      ok = warp_wait(acc_full + 8 * buf, acc.parity, abort_ptr);
       if (split > 1) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
       if (!ok) {
         if (lane == 0) give_up(kErrWaitAccum);
