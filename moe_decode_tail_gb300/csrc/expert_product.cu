@@ -56,7 +56,7 @@ struct Args {
   int64_t R;
   int E, N;
   int w_blocks;        // ceil(D / 128)
-  int w_stages, x_stages;
+  int w_stages;
   unsigned long long stage_wait_ns;
 };
 
@@ -150,17 +150,21 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
       : "memory");
   return all != 0;
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                         unsigned long long limit_ns = kWaitLimitNs) {
-  return mbar_wait(bar, parity, limit_ns, abort_flag);
+// By a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
+  if (limit_ns > 1 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, abort_flag));
 }
-// By a whole warp: its first lane asks (32 lanes asking at once are served one by one), the others get its answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, abort_flag);
-  ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-  __syncwarp();
-  return ok;
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 // A place in a ring of `stages` slots and the parity of its current round (counted, not divided: an integer
@@ -186,6 +190,8 @@ struct Part {
 };
 
 // NT: rows of a tile (the accumulator's columns).
+constexpr int steps_of(int nt) { return nt > 128 ? 4 : 8; }
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -194,24 +200,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kXStage = NT * kXBlock * 2;
   constexpr int kBox = NT < 64 ? NT : 64;          // rows of one TMA box
   constexpr int kAccs = NT > 128 ? 1 : 2;          // accumulators, taken in turn
-  constexpr int kAStages = 8;                      // weight half stages in tensor memory
+  constexpr int kSteps = steps_of(NT);             // ring of MMA steps: 64 of the reduction, A in tensor memory, B beside
   constexpr uint32_t kTmemA = kAccs * NT;          // first column of the A ring
-  static_assert(kTmemA + kAStages * kAColumns <= 512, "tensor memory");
+  static_assert(kTmemA + kSteps * kAColumns <= 512, "tensor memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
   const uint32_t w_ring = base, x_ring = w_ring + (uint32_t)(a.w_stages * kWStage);
-  uint32_t at = x_ring + (uint32_t)(a.x_stages * kXStage);
+  uint32_t at = x_ring + (uint32_t)(kSteps * kXStage);
   auto bars = [&](int n) {
     const uint32_t first = at;
     at += 8u * n;
     return first;
   };
   const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages);
-  const uint32_t x_full = bars(a.x_stages), x_empty = bars(a.x_stages);
-  const uint32_t a_full = bars(kAStages), a_empty = bars(kAStages);
+  const uint32_t x_full = bars(kSteps), step_full = bars(kSteps), step_empty = bars(kSteps);
   const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort, last part
   volatile uint32_t* abort_ptr = word + 1;
@@ -224,13 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(w_full + 8 * s, 1);
       mbar_init(w_empty + 8 * s, kConvertWarps);
     }
-    for (int s = 0; s < a.x_stages; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
       mbar_init(x_full + 8 * s, 1);
-      mbar_init(x_empty + 8 * s, 1);
-    }
-    for (int s = 0; s < kAStages; ++s) {
-      mbar_init(a_full + 8 * s, kConvertWarps / 2);
-      mbar_init(a_empty + 8 * s, 1);
+      mbar_init(step_full + 8 * s, kConvertWarps / 2);
+      mbar_init(step_empty + 8 * s, 1);
     }
     for (int s = 0; s < kAccs; ++s) {
       mbar_init(acc_full + 8 * s, 1);
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
         const Part q = part_of(p);
         for (int i = 0; i < q.blocks; ++i, ++g, w.step(a.w_stages)) {
-          if (!wait_for(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
+          if (!mbar_wait(w_empty + 8 * w.slot, w.parity ^ 1u, kWaitLimitNs, abort_ptr)) {  // the first round finds it free
             give_up(kErrWaitEmpty);
             ok = false;
             break;
@@ -353,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
         const Part q = part_of(p);
         const int boxes = (q.rows + kBox - 1) / kBox;
-        for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(a.x_stages)) {
+        for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(kSteps)) {
           const int s = x.slot;
-          if (!wait_for(x_empty + 8 * s, x.parity ^ 1u, abort_ptr)) {
+          if (!mbar_wait(step_empty + 8 * s, x.parity ^ 1u, kWaitLimitNs, abort_ptr)) {
             give_up(kErrWaitEmpty);
             ok = false;
             break;
@@ -366,59 +368,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (2 * q.k0 + i) * kXBlock, q.r0 + b * kBox, keep);
         }
       }
-      for (int64_t i = g > a.x_stages ? g - a.x_stages : 0; i < g; ++i)
-        if (!mbar_wait(x_full + 8 * (i % a.x_stages), (uint32_t)(i / a.x_stages) & 1u)) raise_error(kErrWaitDrain);
+      for (int64_t i = g > kSteps ? g - kSteps : 0; i < g; ++i)
+        if (!mbar_wait(x_full + 8 * (i % kSteps), (uint32_t)(i / kSteps) & 1u)) raise_error(kErrWaitDrain);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
-      Ring x, w, acc;
-      bool ok = true;
-      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
-        const Part q = part_of(p);
-        const int buf = acc.slot;
-        if (!wait_for(acc_empty + 8 * buf, acc.parity ^ 1u, abort_ptr)) {
-          give_up(kErrWaitAccum);
+    // The whole warp walks the steps, so that the addresses stay in uniform registers, and one lane issues.
+    const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
+    Ring step, acc;
+    bool ok = true;
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
+      const Part q = part_of(p);
+      if (!warp_wait(acc_empty + 8 * acc.slot, acc.parity ^ 1u, abort_ptr)) {
+        if (lane == 0) give_up(kErrWaitAccum);
+        break;
+      }
+      const uint32_t idesc = idesc_f16(kTileM, (q.rows + 15) & ~15);
+      const uint32_t d = tmem + acc.slot * NT;
+      const int steps = 2 * q.blocks;
+      for (int i = 0; i < steps; ++i, step.step(kSteps)) {
+        if (!warp_wait(step_full + 8 * step.slot, step.parity, abort_ptr, limit)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t idesc = idesc_f16(kTileM, (q.rows + 15) & ~15);
-        for (int i = 0; i < 2 * q.blocks; ++i, x.step(a.x_stages), w.step(kAStages)) {
-          const int sx = x.slot, sa = w.slot;
-          if (!wait_for(x_full + 8 * sx, x.parity, abort_ptr, limit) ||
-              !wait_for(a_full + 8 * sa, w.parity, abort_ptr)) {
-            give_up(kErrWaitFull);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bdesc = smem_desc_sw128(x_ring + sx * kXStage);
+        const uint64_t bdesc = smem_desc_sw128(x_ring + step.slot * kXStage);
+        const uint32_t w = tmem + kTmemA + step.slot * kAColumns;
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kXBlock / 16; ++kk)  // 16 FP16: 8 columns of A, 32 bytes along B's swizzled row
-            mma_f16_ts(tmem + buf * NT, tmem + kTmemA + sa * kAColumns + 8 * kk, bdesc + 2 * kk, idesc,
-                       (i > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(a_empty + 8 * sa);
-          mma_commit(x_empty + 8 * sx);
+            mma_f16_ts(d, w + 8 * kk, bdesc + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(step_empty + 8 * step.slot);
+          if (i == steps - 1) mma_commit(acc_full + 8 * acc.slot);
         }
-        if (ok) mma_commit(acc_full + 8 * buf);
+        __syncwarp();
       }
-      mma_commit(mma_done);  // the MMAs that were issued are done before tensor memory is freed
-      if (!mbar_wait(mma_done, 0)) raise_error(kErrWaitAccum);
     }
+    if (elect_one()) mma_commit(mma_done);  // the MMAs that were issued are done before tensor memory is freed
+    __syncwarp();
+    if (lane == 0 && !mbar_wait(mma_done, 0)) raise_error(kErrWaitAccum);
     __syncwarp();
   } else if (warp >= kEpilogueWarps) {
     // ---------------- int8 to FP16: half stage `half` of every weight stage, one TMEM lane a thread ----------------
     const int half = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    Ring w, half_stage;
-    half_stage.slot = half;
+    Ring w, step;
+    step.slot = half;
     bool ok = true;
     for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
       const Part q = part_of(p);
-      for (int i = 0; i < q.blocks; ++i, w.step(a.w_stages), half_stage.step(kAStages, 2)) {
-        const int s = w.slot, sa = half_stage.slot;
+      for (int i = 0; i < q.blocks; ++i, w.step(a.w_stages), step.step(kSteps, 2)) {
+        const int s = w.slot;
         if (!warp_wait(w_full + 8 * s, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
@@ -436,16 +438,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(w_empty + 8 * s);
-        if (!warp_wait(a_empty + 8 * sa, half_stage.parity ^ 1u, abort_ptr)) {
+        if (!warp_wait(step_empty + 8 * step.slot, step.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st32(tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + sa * kAColumns, r);
+        tmem_st32(tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + step.slot * kAColumns, r);
         tc_fence_before();
+        // one warp of the four sees the rows arrive too, so that the MMA warp has one barrier to wait for
+        if (quarter == 0 && !warp_wait(x_full + 8 * step.slot, step.parity, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
+          break;
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + 8 * sa);
+        if (lane == 0) mbar_arrive(step_full + 8 * step.slot);
       }
     }
   } else {
@@ -548,14 +556,14 @@ template <int NT>
 cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
   constexpr int kLimit = 227 * 1024;
   constexpr int kXStage = NT * kXBlock * 2;
-  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (4 * 16 + 2 * 8 + 5);
-  a.x_stages = NT >= 256 ? 4 : 8;
-  a.w_stages = (kLimit - fixed - a.x_stages * kXStage) / kWStage;
+  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 8 + 2 * 2 + 1);
+  constexpr int kSteps = steps_of(NT);
+  a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
   auto kernel = expert_product_kernel<NT>;
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
   if (e != cudaSuccess) return e;
-  const size_t smem = fixed + (size_t)a.x_stages * kXStage + (size_t)a.w_stages * kWStage;
+  const size_t smem = fixed + (size_t)kSteps * kXStage + (size_t)a.w_stages * kWStage;
   return launch_pdl(kernel, dim3(sms), dim3(kThreads), smem, stream, map_w, map_x, a);
 }
 
