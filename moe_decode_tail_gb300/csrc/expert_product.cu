@@ -40,7 +40,8 @@ constexpr int kWBlock = 128;                   // reduction bytes of a weight st
 constexpr int kWStage = kTileM * kWBlock;      // 16 KB
 constexpr int kXBlock = 64;                    // FP16 of a row stage: one swizzle row
 constexpr int kAColumns = kXBlock / 2;         // TMEM columns of a weight half stage: two FP16 each
-constexpr int kEpilogueWarps = 4, kConvertWarps = 8;
+constexpr int kEpilogueWarps = 4, kConvertWarps = 16;  // the latter in sets of four: a warp for each TMEM quarter
+constexpr int kSets = kConvertWarps / 4;
 constexpr int kWarpW = kEpilogueWarps + kConvertWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
 constexpr int kThreads = 32 * (kWarpMma + 1);
 constexpr int kMaxParts = 320;                 // parts (tiles x splits) with FP32 sums in the workspace
@@ -227,11 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.w_stages; ++s) {
       mbar_init(w_full + 8 * s, 1);
-      mbar_init(w_empty + 8 * s, kConvertWarps);
+      mbar_init(w_empty + 8 * s, 8);           // two sets read a stage, a half each
     }
     for (int s = 0; s < kSteps; ++s) {
       mbar_init(x_full + 8 * s, 1);
-      mbar_init(step_full + 8 * s, kConvertWarps / 2);
+      mbar_init(step_full + 8 * s, 4);
       mbar_init(step_empty + 8 * s, 1);
     }
     for (int s = 0; s < kAccs; ++s) {
@@ -322,59 +323,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpW) {
     // ---------------- weight bytes ----------------
-    if (lane == 0) {
-      const uint64_t once = policy_evict_first(), again = policy_evict_last();
-      int64_t g = 0;
-      Ring w;
-      bool ok = true;
-      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
-        const Part q = part_of(p);
-        for (int i = 0; i < q.blocks; ++i, ++g, w.step(a.w_stages)) {
-          if (!mbar_wait(w_empty + 8 * w.slot, w.parity ^ 1u, kWaitLimitNs, abort_ptr)) {  // the first round finds it free
-            give_up(kErrWaitEmpty);
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(w_full + 8 * w.slot, kWStage);
-          tma_load_3d(w_ring + w.slot * kWStage, &map_w, w_full + 8 * w.slot, (q.k0 + i) * kWBlock, q.m0, q.e,
-                      q.shared ? again : once);
+    // The warps that issue copies and MMAs walk their loops whole, so that the addresses stay in uniform
+    // registers, and one lane issues.
+    const uint64_t once = policy_evict_first(), again = policy_evict_last();
+    int64_t g = 0;
+    Ring w;
+    bool ok = true;
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
+      const Part q = part_of(p);
+      const uint64_t policy = q.shared ? again : once;
+      for (int i = 0; i < q.blocks; ++i, ++g, w.step(a.w_stages)) {
+        if (!warp_wait(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
+          if (lane == 0) give_up(kErrWaitEmpty);
+          ok = false;
+          break;
         }
+        if (elect_one()) {
+          mbar_expect_tx(w_full + 8 * w.slot, kWStage);
+          tma_load_3d(w_ring + w.slot * kWStage, &map_w, w_full + 8 * w.slot, (q.k0 + i) * kWBlock, q.m0, q.e, policy);
+        }
+        __syncwarp();
       }
-      for (int64_t i = g > a.w_stages ? g - a.w_stages : 0; i < g; ++i)  // copies in flight land before the block's memory goes away
-        if (!mbar_wait(w_full + 8 * (i % a.w_stages), (uint32_t)(i / a.w_stages) & 1u)) raise_error(kErrWaitDrain);
     }
+    if (lane == 0)
+      for (int64_t i = g > a.w_stages ? g - a.w_stages : 0; i < g; ++i)  // copies in flight land before the block ends
+        if (!mbar_wait(w_full + 8 * (i % a.w_stages), (uint32_t)(i / a.w_stages) & 1u)) raise_error(kErrWaitDrain);
     __syncwarp();
   } else if (warp == kWarpX) {
     // ---------------- FP16 rows ----------------
-    if (lane == 0) {
-      grid_dependency_wait();  // the expand kernel's rows
-      const uint64_t keep = policy_evict_last();
-      int64_t g = 0;
-      Ring x;
-      bool ok = true;
-      for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
-        const Part q = part_of(p);
-        const int boxes = (q.rows + kBox - 1) / kBox;
-        for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(kSteps)) {
-          const int s = x.slot;
-          if (!mbar_wait(step_empty + 8 * s, x.parity ^ 1u, kWaitLimitNs, abort_ptr)) {
-            give_up(kErrWaitEmpty);
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(x_full + 8 * s, (uint32_t)(boxes * kBox * kXBlock * 2));
+    grid_dependency_wait();  // the expand kernel's rows
+    const uint64_t keep = policy_evict_last();
+    int64_t g = 0;
+    Ring x;
+    bool ok = true;
+    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
+      const Part q = part_of(p);
+      const int boxes = NT <= kBox ? 1 : (q.rows + kBox - 1) / kBox;
+      for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(kSteps)) {
+        if (!warp_wait(step_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitEmpty);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          mbar_expect_tx(x_full + 8 * x.slot, (uint32_t)(boxes * kBox * kXBlock * 2));
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(x_ring + s * kXStage + b * kBox * kXBlock * 2, &map_x, x_full + 8 * s,
+            tma_load_2d(x_ring + x.slot * kXStage + b * kBox * kXBlock * 2, &map_x, x_full + 8 * x.slot,
                         (2 * q.k0 + i) * kXBlock, q.r0 + b * kBox, keep);
         }
+        __syncwarp();
       }
+    }
+    if (lane == 0)
       for (int64_t i = g > kSteps ? g - kSteps : 0; i < g; ++i)
         if (!mbar_wait(x_full + 8 * (i % kSteps), (uint32_t)(i / kSteps) & 1u)) raise_error(kErrWaitDrain);
-    }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ---------------- MMA issuer ----------------
-    // The whole warp walks the steps, so that the addresses stay in uniform registers, and one lane issues.
     const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
     Ring step, acc;
     bool ok = true;
@@ -411,15 +416,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && !mbar_wait(mma_done, 0)) raise_error(kErrWaitAccum);
     __syncwarp();
   } else if (warp >= kEpilogueWarps) {
-    // ---------------- int8 to FP16: half stage `half` of every weight stage, one TMEM lane a thread ----------------
-    const int half = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
+    // ---------------- int8 to FP16, one TMEM lane a thread ----------------
+    // Set s takes the MMA steps s, s + kSets, ...: half s % 2 of every (kSets / 2)-th weight stage.
+    const int set = (warp - kEpilogueWarps) >> 2, half = set & 1, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     Ring w, step;
-    step.slot = half;
+    w.step(a.w_stages, set >> 1);
+    step.slot = set % kSteps;
+    step.parity = (uint32_t)(set / kSteps);
+    int ahead = set >> 1;  // weight stages until this set's next one
     bool ok = true;
     for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
       const Part q = part_of(p);
-      for (int i = 0; i < q.blocks; ++i, w.step(a.w_stages), step.step(kSteps, 2)) {
+      for (; ahead < q.blocks; ahead += kSets / 2, w.step(a.w_stages, kSets / 2), step.step(kSteps, kSets)) {
         const int s = w.slot;
         if (!warp_wait(w_full + 8 * s, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
@@ -455,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(step_full + 8 * step.slot);
       }
+      ahead -= q.blocks;
     }
   } else {
     // ---------------- accumulators to BF16 ----------------
