@@ -16,8 +16,10 @@
 //            the FP16 rows arrive by TMA as the B operand; four warps read finished accumulators, scale them and
 //            write BF16.  Warp roles meet at mbarriers only, so the weight stream runs on across tiles.
 //
-// Where the tiles are too few for the SMs, each is split along the reduction; a part's FP32 sums go to the
-// workspace and the block that finishes a tile's last part adds them, in the order of the parts.
+// The tiles that are no multiple of the thread blocks (with few rows, all of them) are dealt out by reduction
+// blocks, the same number to each thread block, so such a tile may begin in one and end in another.  A part's FP32
+// sums go to the workspace, and the thread block that finishes a tile's last missing part adds them, in the order
+// of the reduction.  The other tiles follow whole, neighbours at the same time, so that they share what L2 holds.
 //
 // Every wait is bounded in time; on expiry the kernel raises a bit in the device error word, lets its copies and
 // MMAs finish, frees its tensor memory and returns.
@@ -44,16 +46,16 @@ constexpr int kEpilogueWarps = 4, kConvertWarps = 16;  // the latter in sets of 
 constexpr int kSets = kConvertWarps / 4;
 constexpr int kWarpW = kEpilogueWarps + kConvertWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
 constexpr int kThreads = 32 * (kWarpMma + 1);
-constexpr int kMaxParts = 320;                 // parts (tiles x splits) with FP32 sums in the workspace
-constexpr int kMaxSplit = 8;
+constexpr int kMaxGrid = 160;                  // thread blocks: each has at most two parts of a tile
+constexpr int kLeastBlocks = 4;                // reduction blocks a thread block is worth
 
 struct Args {
   const float* x_scale;
   const float* w_scale;
   const int32_t* offsets;
   uint16_t* out;
-  float* partial;      // [kMaxParts][NT][128]
-  unsigned* counters;  // [kMaxParts]: finished parts of a tile, zeroed by the expand kernel
+  float* partial;      // [2 kMaxGrid][NT][128]: a block's continued tile, then the one it begins and does not end
+  unsigned* counters;  // [kMaxGrid]: finished parts of the tile that a block begins, zeroed by the expand kernel
   int64_t R;
   int E, N;
   int w_blocks;        // ceil(D / 128)
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint1
   // weights, scales and offsets at once and wait for this kernel before they touch what it writes.
   launch_dependents();
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kMaxParts; i += blockDim.x) counters[i] = 0;
+    for (int i = threadIdx.x; i < kMaxGrid; i += blockDim.x) counters[i] = 0;
   const int64_t rows = offsets ? clamp_row(offsets[E], R) : R;
   const int64_t n = rows * D / 16;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
@@ -186,12 +188,14 @@ struct Ring {
 
 // A part: reduction blocks [k0, k0 + blocks) of 128 channels from m0 by rows [r0, r0 + rows) of expert e.
 struct Part {
-  int e, m0, r0, rows, k0, blocks, tile;
+  int e, m0, r0, rows, k0, blocks;
+  int64_t tile;
   bool shared;  // more than one row tile reads this expert's weights
 };
 
 // NT: rows of a tile (the accumulator's columns).
-constexpr int steps_of(int nt) { return nt > 128 ? 4 : 8; }
+// What tensor memory has beside the accumulators, in steps; with 256 rows shared memory is the limit.
+constexpr int steps_of(int nt) { return nt > 128 ? 4 : (512 - 2 * nt) / kAColumns; }
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -277,26 +281,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   const int m_tiles = (a.N + kTileM - 1) / kTileM;
+  // Tiles in the order (expert, channel tile, row tile).  The first `dealt` are dealt out by reduction blocks,
+  // [my_begin, my_end) of them to this thread block; then come whole tiles, one in gridDim.x.
   const int64_t tiles = (int64_t)s_first[a.E] * m_tiles;
-  // Parts of a tile: the split with the least work in a row for a block, a part's fixed cost counted as two
-  // reduction blocks.
-  int split = 1;
-  {
-    int64_t least = (tiles + gridDim.x - 1) / gridDim.x * (a.w_blocks + 2);
-    for (int s = 2; s <= kMaxSplit && s <= a.w_blocks && tiles * s <= kMaxParts; ++s) {
-      const int64_t cost = (tiles * s + gridDim.x - 1) / gridDim.x * ((a.w_blocks + s - 1) / s + 2);
-      if (cost < least) {
-        least = cost;
-        split = s;
-      }
+  // Dealing saves the idle part of a last wave, w_blocks * (1 - odd / grid) reduction blocks, and costs the FP32
+  // sums' way through memory: about one reduction block's time for 16 rows.
+  const int odd = (int)(tiles % gridDim.x);
+  const int64_t dealt = (int64_t)a.w_blocks * (gridDim.x - odd) > (int64_t)(NT / 16) * gridDim.x ? odd : 0;
+  const int64_t total = dealt * a.w_blocks;
+  const int64_t worth = (total + kLeastBlocks - 1) / kLeastBlocks;
+  const int64_t grid = worth < gridDim.x ? worth : gridDim.x;  // thread blocks with dealt work
+  const int64_t my_begin = blockIdx.x < grid ? blockIdx.x * total / grid : 0;
+  const int64_t my_end = blockIdx.x < grid ? (blockIdx.x + 1) * total / grid : 0;
+  auto owner = [&](int64_t b) { return (int)(((b + 1) * grid + total - 1) / total) - 1; };  // the block that has b
+  struct Walk {  // of this thread block's parts: the next dealt reduction block, the next whole tile
+    int64_t dealt, tile;
+  };
+  const Walk start = {my_begin, dealt + blockIdx.x};
+  auto next_part = [&](Walk& at, Part& q) {
+    int64_t tile;
+    if (at.dealt < my_end) {
+      tile = at.dealt / a.w_blocks;
+      q.k0 = (int)(at.dealt - tile * a.w_blocks);
+      q.blocks = (int)min((int64_t)(a.w_blocks - q.k0), my_end - at.dealt);
+      at.dealt += q.blocks;
+    } else if (at.tile < tiles) {
+      tile = at.tile;
+      q.k0 = 0;
+      q.blocks = a.w_blocks;
+      at.tile += gridDim.x;
+    } else {
+      return false;
     }
-  }
-  const int64_t parts = tiles * split;
-  // Parts in the order (expert, channel tile, row tile, split): neighbours share a weight tile.
-  auto part_of = [&](int64_t p) {
-    Part q;
-    const int64_t tile = p / split;
-    const int s = (int)(p - tile * split);
     int lo = 0, hi = a.E - 1;  // the last expert whose tiles start at or before this one
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -310,11 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     q.m0 = m * kTileM;
     q.r0 = s_row[lo] + t * NT;
     q.rows = min(NT, s_count[lo] - t * NT);
-    q.k0 = (int)((int64_t)s * a.w_blocks / split);
-    q.blocks = (int)((int64_t)(s + 1) * a.w_blocks / split) - q.k0;
-    q.tile = (int)(split > 1 ? tile : 0);
+    q.tile = tile;
     q.shared = row_tiles > 1;
-    return q;
+    return true;
   };
   auto give_up = [&](unsigned bit) {
     if (!*abort_ptr) raise_error(bit);
@@ -329,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t g = 0;
     Ring w;
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
-      const Part q = part_of(p);
+    Part q;
+    for (Walk at = start; ok && next_part(at, q);) {
       const uint64_t policy = q.shared ? again : once;
       for (int i = 0; i < q.blocks; ++i, ++g, w.step(a.w_stages)) {
         if (!warp_wait(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
@@ -356,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t g = 0;
     Ring x;
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
-      const Part q = part_of(p);
+    Part q;
+    for (Walk at = start; ok && next_part(at, q);) {
       const int boxes = NT <= kBox ? 1 : (q.rows + kBox - 1) / kBox;
       for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(kSteps)) {
         if (!warp_wait(step_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
@@ -367,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) {
           mbar_expect_tx(x_full + 8 * x.slot, (uint32_t)(boxes * kBox * kXBlock * 2));
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(x_ring + x.slot * kXStage + b * kBox * kXBlock * 2, &map_x, x_full + 8 * x.slot,
-                        (2 * q.k0 + i) * kXBlock, q.r0 + b * kBox, keep);
+          for (int c = 0; c < boxes; ++c)
+            tma_load_2d(x_ring + x.slot * kXStage + c * kBox * kXBlock * 2, &map_x, x_full + 8 * x.slot,
+                        (2 * q.k0 + i) * kXBlock, q.r0 + c * kBox, keep);
         }
         __syncwarp();
       }
@@ -383,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
     Ring step, acc;
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
-      const Part q = part_of(p);
+    Part q;
+    for (Walk at = start; ok && next_part(at, q); acc.step(kAccs)) {
       if (!warp_wait(acc_empty + 8 * acc.slot, acc.parity ^ 1u, abort_ptr)) {
         if (lane == 0) give_up(kErrWaitAccum);
         break;
@@ -426,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     step.parity = (uint32_t)(set / kSteps);
     int ahead = set >> 1;  // weight stages until this set's next one
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x) {
-      const Part q = part_of(p);
+    Part q;
+    for (Walk at = start; ok && next_part(at, q);) {
       for (; ahead < q.blocks; ahead += kSets / 2, w.step(a.w_stages, kSets / 2), step.step(kSteps, kSets)) {
         const int s = w.slot;
         if (!warp_wait(w_full + 8 * s, w.parity, abort_ptr)) {
@@ -471,20 +485,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependency_wait();  // the counters
     Ring acc;
     bool ok = true;
-    for (int64_t p = blockIdx.x; ok && p < parts; p += gridDim.x, acc.step(kAccs)) {
-      const Part q = part_of(p);
+    Part q;
+    for (Walk at = start; ok && next_part(at, q); acc.step(kAccs)) {
       const int buf = acc.slot;
       const int n = q.m0 + warp * 32 + lane;
       const float ws = n < a.N ? a.w_scale[(int64_t)q.e * a.N + n] : 0.0f;
       ok = warp_wait(acc_full + 8 * buf, acc.parity, abort_ptr);
-      if (split > 1) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
+      const bool whole = q.blocks == a.w_blocks;
+      if (!whole) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
       if (!ok) {
         if (lane == 0) give_up(kErrWaitAccum);
         break;
       }
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(warp * 32) << 16) + buf * NT;
-      float* mine = split > 1 ? a.partial + (int64_t)p * NT * kTileM + warp * 32 + lane : nullptr;
+      // FP32 sums [row][channel] of thread block c's part of a tile, this thread's channel
+      auto sums = [&](int c, bool begins) {
+        return a.partial + (int64_t)(2 * c + (begins ? 1 : 0)) * NT * kTileM + warp * 32 + lane;
+      };
+      float* mine = sums(blockIdx.x, q.k0 == 0);
       auto finish16 = [&](const float (&v)[16], int c) {
         const int r = c + (lane & 15);
         const float xs = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < q.rows; c += 16) {
         float v[16];
         tmem_ld16(src + c, v);
-        if (split == 1) {
+        if (whole) {
           finish16(v, c);
         } else {
 #pragma unroll
@@ -509,22 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
-      if (split > 1) {
+      if (!whole) {
+        const int first = owner(q.tile * a.w_blocks), last = owner((q.tile + 1) * a.w_blocks - 1);
         __threadfence();
         epilogue_all(true);
-        if (threadIdx.x == 0) word[2] = atomicAdd(&a.counters[q.tile], 1u);
+        if (threadIdx.x == 0) word[2] = atomicAdd(&a.counters[first], 1u);
         epilogue_all(true);
-        if (word[2] == (unsigned)(split - 1)) {  // the tile's last part: add them all, in order
+        if (word[2] == (unsigned)(last - first)) {  // the tile's last missing part: add them all, in order
           __threadfence();
-          const float* first = a.partial + (int64_t)q.tile * split * NT * kTileM + warp * 32 + lane;
 #pragma unroll 1
           for (int c = 0; c < q.rows; c += 16) {
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            for (int s = 0; s < split; ++s) {
+            for (int s = first; s <= last; ++s) {
+              const float* theirs = sums(s, s == first) + c * kTileM;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __ldcg(first + ((int64_t)s * NT + c + i) * kTileM);
+              for (int i = 0; i < 16; ++i) v[i] += __ldcg(theirs + i * kTileM);
             }
             finish16(v, c);
           }
@@ -557,8 +577,8 @@ Layout layout(int64_t R, int E, int D) {
   Layout l;
   l.x16 = 0;
   l.counters = round_up((size_t)R * D * 2, 256);
-  l.partial = l.counters + round_up(kMaxParts * 4, 256);
-  l.bytes = l.partial + (size_t)kMaxParts * kTileM * rows_of_tile(R, E) * 4;
+  l.partial = l.counters + round_up(kMaxGrid * 4, 256);
+  l.bytes = l.partial + (size_t)2 * kMaxGrid * kTileM * rows_of_tile(R, E) * 4;
   return l;
 }
 
@@ -566,7 +586,7 @@ template <int NT>
 cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
   constexpr int kLimit = 227 * 1024;
   constexpr int kXStage = NT * kXBlock * 2;
-  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 8 + 2 * 2 + 1);
+  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
   constexpr int kSteps = steps_of(NT);
   a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
@@ -574,7 +594,7 @@ cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& 
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
   if (e != cudaSuccess) return e;
   const size_t smem = fixed + (size_t)kSteps * kXStage + (size_t)a.w_stages * kWStage;
-  return launch_pdl(kernel, dim3(sms), dim3(kThreads), smem, stream, map_w, map_x, a);
+  return launch_pdl(kernel, dim3(sms < kMaxGrid ? sms : kMaxGrid), dim3(kThreads), smem, stream, map_w, map_x, a);
 }
 
 }  // namespace
