@@ -42,7 +42,7 @@ constexpr int kWBlock = 128;                   // reduction bytes of a weight st
 constexpr int kWStage = kTileM * kWBlock;      // 16 KB
 constexpr int kXBlock = 64;                    // FP16 of a row stage: one swizzle row
 constexpr int kAColumns = kXBlock / 2;         // TMEM columns of a weight half stage: two FP16 each
-constexpr int kEpilogueWarps = 4, kConvertWarps = 16;  // the latter in sets of four: a warp for each TMEM quarter
+constexpr int kEpilogueWarps = 4, kConvertWarps = 8;  // the latter in sets of four: a warp for each TMEM quarter
 constexpr int kSets = kConvertWarps / 4;
 constexpr int kWarpW = kEpilogueWarps + kConvertWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
 constexpr int kThreads = 32 * (kWarpMma + 1);
@@ -541,10 +541,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            for (int s = first; s <= last; ++s) {
-              const float* theirs = sums(s, s == first) + c * kTileM;
+            for (int s = first; s <= last; s += 3) {  // three parts' loads in flight
+              float u[3][16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __ldcg(theirs + i * kTileM);
+              for (int k = 0; k < 3; ++k) {
+                const float* theirs = sums(min(s + k, last), s + k == first) + c * kTileM;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[k][i] = s + k <= last ? __ldcg(theirs + i * kTileM) : 0.0f;
+              }
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += u[k][i];
             }
             finish16(v, c);
           }
