@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
   const int e = threadIdx.x;  // E <= 1024
   int total = 0, before = 0;
   if (e < a.E) {
+#pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
       const int n = s_mem[w * a.E + e];
       s_mem[w * a.E + e] = total;
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
     }
     if (gridDim.x > 1) {
       total = 0;
+#pragma unroll 8
       for (int c = 0; c < (int)gridDim.x; ++c) {
         const int n = a.counts[(int64_t)c * a.E + e];
         if (c < (int)blockIdx.x) before += n;
@@ -157,32 +159,65 @@ __device__ __forceinline__ float route_weight(const void* w, int64_t i) {
   return static_cast<const float*>(w)[i];
 }
 
+// A route's row (or -1) and weight, kept by the lane of its number: lane k holds route k of token t.
+struct Route {
+  int row;
+  float w;
+};
 template <int WMODE>
-__global__ void __launch_bounds__(256) combine_rows_kernel(const CombineArgs a) {
+__device__ __forceinline__ Route route_of_lane(const CombineArgs& a, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  Route r = {-1, 0.0f};
+  if (lane < a.K) {
+    r.row = a.idx[t * a.K + lane];
+    r.w = route_weight<WMODE>(a.w, t * a.K + lane);
+    if (r.row >= a.num_rows) r.row = -1;
+  }
+  return r;
+}
+
+constexpr int kRoutesAtOnce = 8;  // rows in flight of a thread
+constexpr int kCombineThreads = 64;
+
+template <int WMODE>
+__global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const CombineArgs a) {
   grid_dependency_wait();
   launch_dependents();
   const int64_t t = blockIdx.x;
   const int nv = a.H >> 3;
-  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
-    float acc[8];
+  const int v = blockIdx.y * blockDim.x + threadIdx.x;
+  const Route mine = route_of_lane<WMODE>(a, t);
+  float acc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < a.K; ++k) {
-      const int64_t j = a.idx[t * a.K + k];
-      if (j < 0 || j >= a.num_rows) continue;
-      const float w = route_weight<WMODE>(a.w, t * a.K + k);
-      float f[8];
-      unpack8(ld_stream_v4(a.rows + j * a.H + 8 * v), f);
+  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+  unsigned left = __ballot_sync(0xffffffffu, mine.row >= 0);  // routes with a row, in order
+  while (left) {
+    uint4 d[kRoutesAtOnce];
+    float w[kRoutesAtOnce];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += w * f[e];
+    for (int i = 0; i < kRoutesAtOnce; ++i) {
+      const int k = left ? __ffs(left) - 1 : 0;
+      const int j = __shfl_sync(0xffffffffu, mine.row, k);
+      w[i] = __shfl_sync(0xffffffffu, mine.w, k);
+      d[i] = make_uint4(0, 0, 0, 0);
+      if (left == 0) w[i] = 0.0f;  // no route: zeros times zero
+      else if (v < nv) d[i] = ld_stream_v4(a.rows + (int64_t)j * a.H + 8 * v);
+      left &= left - 1;
     }
+#pragma unroll
+    for (int i = 0; i < kRoutesAtOnce; ++i) {
+      float f[8];
+      unpack8(d[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += w[i] * f[e];
+    }
+  }
+  if (v < nv)
     st_v4(a.out + t * a.H + 8 * v, make_uint4(pack_bf16x2_pz(acc[0], acc[1]), pack_bf16x2_pz(acc[2], acc[3]),
                                               pack_bf16x2_pz(acc[4], acc[5]), pack_bf16x2_pz(acc[6], acc[7])));
-  }
 }
 
-// A block per token: d_out's row stays in registers while the routes' rows pass.
+// A block per token: d_out's row stays in registers while the routes' rows pass, the next route's loads in flight.
 template <int WMODE, int VPT>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineArgs a) {
   __shared__ float s_dot[kMaxK][32];
@@ -190,28 +225,44 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineArgs a)
   launch_dependents();
   const int64_t t = blockIdx.x;
   const int nv = a.H >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint4 d[VPT];
+  const Route mine = route_of_lane<WMODE>(a, t);
+  uint4 d[VPT], next[VPT];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (j >= 0 && v < nv) next[i] = ld_stream_v4(a.rows + (int64_t)j * a.H + 8 * v);
+    }
+  };
+  int j = __shfl_sync(0xffffffffu, mine.row, 0);
+  load(j);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v < nv) d[i] = ld_stream_v4(a.d_out + t * a.H + 8 * v);
   }
   for (int k = 0; k < a.K; ++k) {
-    const int64_t j = a.idx[t * a.K + k];
-    const bool live = j >= 0 && j < a.num_rows;
+    uint4 row[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) row[i] = next[i];
+    const int here = j;
+    const float w = __shfl_sync(0xffffffffu, mine.w, k);
+    if (k + 1 < a.K) {
+      j = __shfl_sync(0xffffffffu, mine.row, k + 1);
+      load(j);
+    }
     float dot = 0.0f;
-    if (live) {
-      const float w = route_weight<WMODE>(a.w, t * a.K + k);
+    if (here >= 0) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v >= nv) continue;
         float f[8], g[8];
-        unpack8(ld_stream_v4(a.rows + j * a.H + 8 * v), f);
+        unpack8(row[i], f);
         unpack8(d[i], g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dot += f[e] * g[e];
-        st_v4(a.d_rows + j * a.H + 8 * v,
+        st_v4(a.d_rows + (int64_t)here * a.H + 8 * v,
               make_uint4(pack_bf16x2_pz(w * g[0], w * g[1]), pack_bf16x2_pz(w * g[2], w * g[3]),
                          pack_bf16x2_pz(w * g[4], w * g[5]), pack_bf16x2_pz(w * g[6], w * g[7])));
       }
@@ -252,18 +303,26 @@ cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t st
 
 cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
   const int nv = a.H >> 3;
-  const dim3 grid(a.b, (nv + 255) / 256);
-  if (wmode == kWeightUnit) return launch_pdl(combine_rows_kernel<kWeightUnit>, grid, dim3(256), 0, stream, a);
-  if (wmode == kWeightBF16) return launch_pdl(combine_rows_kernel<kWeightBF16>, grid, dim3(256), 0, stream, a);
-  return launch_pdl(combine_rows_kernel<kWeightF32>, grid, dim3(256), 0, stream, a);
+  // Small blocks: 64 threads took 83 us where 256 took 86 (8191 tokens, 16 routes, 3584 columns), and at 64 tokens
+  // they spread a row over more SMs.
+  const int threads = kCombineThreads;
+  const dim3 grid(a.b, (nv + threads - 1) / threads);
+  if (wmode == kWeightUnit) return launch_pdl(combine_rows_kernel<kWeightUnit>, grid, dim3(threads), 0, stream, a);
+  if (wmode == kWeightBF16) return launch_pdl(combine_rows_kernel<kWeightBF16>, grid, dim3(threads), 0, stream, a);
+  return launch_pdl(combine_rows_kernel<kWeightF32>, grid, dim3(threads), 0, stream, a);
 }
 
 cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
   const int nv = a.H >> 3;
-  const int threads = ((nv + 3) / 4 + 31) / 32 * 32;
+  // Two vectors a thread: 96 us for 4096 tokens, 8 routes, 4096 columns; one or four: 103 and 104.  More only where
+  // a block of 1024 threads needs them.
+  const int vpt = nv <= 2048 ? 2 : 4;
+  const dim3 threads(((nv + vpt - 1) / vpt + 31) / 32 * 32);
   if (wmode == kWeightBF16)
-    return launch_pdl(combine_grad_kernel<kWeightBF16, 4>, dim3(a.b), dim3(threads), 0, stream, a);
-  return launch_pdl(combine_grad_kernel<kWeightF32, 4>, dim3(a.b), dim3(threads), 0, stream, a);
+    return vpt == 2 ? launch_pdl(combine_grad_kernel<kWeightBF16, 2>, dim3(a.b), threads, 0, stream, a)
+                    : launch_pdl(combine_grad_kernel<kWeightBF16, 4>, dim3(a.b), threads, 0, stream, a);
+  return vpt == 2 ? launch_pdl(combine_grad_kernel<kWeightF32, 2>, dim3(a.b), threads, 0, stream, a)
+                  : launch_pdl(combine_grad_kernel<kWeightF32, 4>, dim3(a.b), threads, 0, stream, a);
 }
 
 }  // namespace moetail
