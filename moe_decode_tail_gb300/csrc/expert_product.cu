@@ -80,6 +80,8 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t v, uint32_t& lo, uint32_t
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+constexpr int kExpand = 4;  // loads of a thread in flight
+
 __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint16_t* x16, const int32_t* offsets, int E,
                                                           int64_t R, int D, unsigned* counters) {
   grid_dependency_wait();
@@ -90,15 +92,23 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint1
     for (int i = threadIdx.x; i < kMaxGrid; i += blockDim.x) counters[i] = 0;
   const int64_t rows = offsets ? clamp_row(offsets[E], R) : R;
   const int64_t n = rows * D / 16;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(x + 16 * i);
-    uint4 a, b;
-    int8x4_to_f16(v.x, a.x, a.y);
-    int8x4_to_f16(v.y, a.z, a.w);
-    int8x4_to_f16(v.z, b.x, b.y);
-    int8x4_to_f16(v.w, b.z, b.w);
-    st_v4(x16 + 16 * i, a);
-    st_v4(x16 + 16 * i + 8, b);
+  for (int64_t i0 = (int64_t)blockIdx.x * (kExpand * 256) + threadIdx.x; i0 < n; i0 += (int64_t)gridDim.x * (kExpand * 256)) {
+    uint4 v[kExpand];
+#pragma unroll
+    for (int j = 0; j < kExpand; ++j)
+      if (i0 + 256 * j < n) v[j] = ld_stream_v4(x + 16 * (i0 + 256 * j));
+#pragma unroll
+    for (int j = 0; j < kExpand; ++j) {
+      const int64_t i = i0 + 256 * j;
+      if (i >= n) break;
+      uint4 a, b;
+      int8x4_to_f16(v[j].x, a.x, a.y);
+      int8x4_to_f16(v[j].y, a.z, a.w);
+      int8x4_to_f16(v[j].z, b.x, b.y);
+      int8x4_to_f16(v[j].w, b.z, b.w);
+      st_v4(x16 + 16 * i, a);
+      st_v4(x16 + 16 * i + 8, b);
+    }
   }
 }
 
@@ -138,6 +148,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// Two values in BF16 (nearest even), -0 made +0: the sum with +0 is exact but for that.
+__device__ __forceinline__ uint32_t bf16x2_pz(float lo, float hi) {
+  const __nv_bfloat162 v = __hadd2(__floats2bfloat162_rn(lo, hi), __floats2bfloat162_rn(0.0f, 0.0f));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Barrier 1 over the four epilogue warps; whether `ok` holds in all of them.
@@ -195,7 +211,7 @@ struct Part {
 
 // NT: rows of a tile (the accumulator's columns).
 // What tensor memory has beside the accumulators, in steps; with 256 rows shared memory is the limit.
-constexpr int steps_of(int nt) { return nt > 128 ? 4 : (512 - 2 * nt) / kAColumns; }
+constexpr int steps_of(int nt) { return nt > 128 ? 5 : (512 - 2 * nt) / kAColumns; }
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -223,9 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages);
   const uint32_t x_full = bars(kSteps), step_full = bars(kSteps), step_empty = bars(kSteps);
   const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
+  at = (at + 15u) & ~15u;
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort, last part
   volatile uint32_t* abort_ptr = word + 1;
-  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16);  // [E + 1] row tiles before an expert
+  const uint32_t scale_addr = at + 16 + (warp & 3) * NT * 4;  // [NT] floats, an epilogue warp's own
+  float* s_scale = reinterpret_cast<float*>(base_ptr + (scale_addr - base));
+  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16 + 16 * NT);  // [E + 1] row tiles before an expert
   int32_t* s_row = s_first + a.E + 1;                                          // [E] an expert's first row
   int32_t* s_count = s_row + a.E;                                              // [E] its rows
 
@@ -324,8 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = left / row_tiles, t = left - m * row_tiles;
     q.e = lo;
     q.m0 = m * kTileM;
-    q.r0 = s_row[lo] + t * NT;
-    q.rows = min(NT, s_count[lo] - t * NT);
+    // an expert's row tiles are equal but for a few rows
+    const int share = ((s_count[lo] + row_tiles - 1) / row_tiles + 15) & ~15;
+    q.r0 = s_row[lo] + t * share;
+    q.rows = min(share, s_count[lo] - t * share);  // at least one: NT * (row_tiles - 1) < s_count
     q.tile = tile;
     q.shared = row_tiles > 1;
     return true;
@@ -489,7 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (Walk at = start; ok && next_part(at, q); acc.step(kAccs)) {
       const int buf = acc.slot;
       const int n = q.m0 + warp * 32 + lane;
+      // the scales, while the MMAs run
       const float ws = n < a.N ? a.w_scale[(int64_t)q.e * a.N + n] : 0.0f;
+      for (int r = lane; r < NT; r += 32) s_scale[r] = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
+      __syncwarp();
       ok = warp_wait(acc_full + 8 * buf, acc.parity, abort_ptr);
       const bool whole = q.blocks == a.w_blocks;
       if (!whole) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
@@ -505,13 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float* mine = sums(blockIdx.x, q.k0 == 0);
       auto finish16 = [&](const float (&v)[16], int c) {
-        const int r = c + (lane & 15);
-        const float xs = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
+        if (n >= a.N) return;
+        uint16_t* out = a.out + (int64_t)(q.r0 + c) * a.N + n;
+        const int rows = q.rows - c;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float s = __shfl_sync(0xffffffffu, xs, i);
-          if (c + i < q.rows && n < a.N)
-            a.out[(int64_t)(q.r0 + c + i) * a.N + n] = (uint16_t)bf16_bits_pz(v[i] * ws * s);
+        for (int i = 0; i < 16; i += 4) {
+          const uint4 s = ld_shared_v4(scale_addr + 4 * (c + i));
+          const float sc[4] = {__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w)};
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const uint32_t two = bf16x2_pz(v[i + j] * ws * sc[j], v[i + j + 1] * ws * sc[j + 1]);
+            if (i + j < rows) out[(int64_t)(i + j) * a.N] = (uint16_t)two;
+            if (i + j + 1 < rows) out[(int64_t)(i + j + 1) * a.N] = (uint16_t)(two >> 16);
+          }
         }
       };
 #pragma unroll 1
@@ -541,16 +571,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            for (int s = first; s <= last; s += 3) {  // three parts' loads in flight
-              float u[3][16];
+            for (int s = first; s <= last; s += 2) {  // two parts' loads in flight
+              float u[2][16];
 #pragma unroll
-              for (int k = 0; k < 3; ++k) {
+              for (int k = 0; k < 2; ++k) {
                 const float* theirs = sums(min(s + k, last), s + k == first) + c * kTileM;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) u[k][i] = s + k <= last ? __ldcg(theirs + i * kTileM) : 0.0f;
               }
 #pragma unroll
-              for (int k = 0; k < 3; ++k)
+              for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] += u[k][i];
             }
@@ -594,7 +624,7 @@ template <int NT>
 cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
   constexpr int kLimit = 227 * 1024;
   constexpr int kXStage = NT * kXBlock * 2;
-  const int fixed = 1024 + 16 + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
+  const int fixed = 1024 + 32 + 16 * NT + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
   constexpr int kSteps = steps_of(NT);
   a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
@@ -628,7 +658,7 @@ cudaError_t launch_expert_product(const ProductArgs& p, const CUtensorMap& map_w
   a.w_blocks = (p.D + kWBlock - 1) / kWBlock;
   a.stage_wait_ns = stage_wait_limit_ns();
   const int64_t vectors = p.R * p.D / 16;
-  const int64_t blocks = (vectors + 255) / 256;
+  const int64_t blocks = (vectors + 256 * kExpand - 1) / (256 * kExpand);
   cudaError_t e = launch_pdl(expand_rows_kernel, dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, stream,
                              p.x, reinterpret_cast<uint16_t*>(ws + l.x16), p.offsets, p.E, p.R, p.D, a.counters);
   if (e != cudaSuccess) return e;
