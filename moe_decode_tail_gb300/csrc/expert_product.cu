@@ -42,10 +42,7 @@ constexpr int kWBlock = 128;                   // reduction bytes of a weight st
 constexpr int kWStage = kTileM * kWBlock;      // 16 KB
 constexpr int kXBlock = 64;                    // FP16 of a row stage: one swizzle row
 constexpr int kAColumns = kXBlock / 2;         // TMEM columns of a weight half stage: two FP16 each
-constexpr int kEpilogueWarps = 4, kConvertWarps = 8;  // the latter in sets of four: a warp for each TMEM quarter
-constexpr int kSets = kConvertWarps / 4;
-constexpr int kWarpW = kEpilogueWarps + kConvertWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
-constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kSets = 2;                       // sets of four converting warps, a warp for each TMEM quarter
 constexpr int kMaxGrid = 160;                  // thread blocks: each has at most two parts of a tile
 constexpr int kLeastBlocks = 4;                // reduction blocks a thread block is worth
 
@@ -128,7 +125,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// 32 consecutive TMEM columns of this thread's lane.
+// 32 consecutive TMEM columns of this thread's lane (to be waited for).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -139,8 +136,30 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// 16 consecutive accumulator columns of this thread's lane: asked for, and there.
+__device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_end(uint32_t (&r)[16], float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+// A barrier over the four warps of an epilogue set.
+__device__ __forceinline__ void set_bar(int set) { asm volatile("bar.sync %0, 128;" ::"r"(2 + set) : "memory"); }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             uint64_t policy) {
   asm volatile(
@@ -156,16 +175,17 @@ __device__ __forceinline__ uint32_t bf16x2_pz(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Barrier 1 over the four epilogue warps; whether `ok` holds in all of them.
-__device__ __forceinline__ bool epilogue_all(bool ok) {
+// Barrier 1 over `threads`; whether `ok` holds in all of them.
+template <int THREADS>
+__device__ __forceinline__ bool all_of(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "n"(THREADS)
       : "memory");
   return all != 0;
 }
@@ -210,20 +230,31 @@ struct Part {
 };
 
 // NT: rows of a tile (the accumulator's columns).
-// What tensor memory has beside the accumulators, in steps; with 256 rows shared memory is the limit.
-constexpr int steps_of(int nt) { return nt > 128 ? 5 : (512 - 2 * nt) / kAColumns; }
+// A step of the MMA warp takes `halves` of a weight stage, 64 of the reduction each: what a step costs besides its
+// MMAs (a wait, a commit) is then paid half as often.  With 256 rows shared memory has no room for two.
+constexpr int halves_of(int nt) { return nt > 128 ? 1 : 2; }
+// Steps in flight: what tensor memory has beside the accumulators; with 256 rows shared memory is the limit.
+constexpr int steps_of(int nt) { return nt > 128 ? 5 : (512 - 2 * nt) / (2 * kAColumns); }
+constexpr int readers_of(int nt) { return nt > 128 ? 2 : 1; }  // sets of four epilogue warps (one accumulator: it waits)
+constexpr int threads_of(int nt) { return 32 * (4 * readers_of(nt) + 4 * kSets + 3); }
+constexpr int kRun = 16;                             // accumulator columns (rows of the result) written at a time
+constexpr int kStaging = kRun * kTileM * 2;          // their BF16, of a set
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(NT), 1)
     expert_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                           const Args a) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kXStage = NT * kXBlock * 2;
+  constexpr int kReaders = readers_of(NT), kEpilogueWarps = 4 * kReaders, kThreads = threads_of(NT);
+  constexpr int kWarpW = kEpilogueWarps + 4 * kSets, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
+  constexpr int kHalves = halves_of(NT), kStepsOfStage = 2 / kHalves;
+  constexpr int kXHalf = NT * kXBlock * 2, kXStage = kHalves * kXHalf;
+  constexpr int kStepColumns = kHalves * kAColumns;  // of A in tensor memory
   constexpr int kBox = NT < 64 ? NT : 64;          // rows of one TMA box
   constexpr int kAccs = NT > 128 ? 1 : 2;          // accumulators, taken in turn
-  constexpr int kSteps = steps_of(NT);             // ring of MMA steps: 64 of the reduction, A in tensor memory, B beside
+  constexpr int kSteps = steps_of(NT);             // ring of MMA steps: A in tensor memory, B in shared memory
   constexpr uint32_t kTmemA = kAccs * NT;          // first column of the A ring
-  static_assert(kTmemA + kSteps * kAColumns <= 512, "tensor memory");
+  static_assert(kTmemA + kSteps * kStepColumns <= 512, "tensor memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
@@ -242,16 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   at = (at + 15u) & ~15u;
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort, last part
   volatile uint32_t* abort_ptr = word + 1;
-  const uint32_t scale_addr = at + 16 + (warp & 3) * NT * 4;  // [NT] floats, an epilogue warp's own
-  float* s_scale = reinterpret_cast<float*>(base_ptr + (scale_addr - base));
-  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16 + 16 * NT);  // [E + 1] row tiles before an expert
-  int32_t* s_row = s_first + a.E + 1;                                          // [E] an expert's first row
-  int32_t* s_count = s_row + a.E;                                              // [E] its rows
+  // an epilogue warp's scales of the rows it writes [NT / kReaders], and its set's BF16 [kRun][128]
+  const uint32_t scales = at + 16 + (warp % kEpilogueWarps) * (NT / kReaders) * 4;
+  float* s_scale = reinterpret_cast<float*>(base_ptr + (scales - base));
+  const uint32_t staging = at + 16 + 16 * NT + (warp >> 2) % kReaders * kStaging;
+  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16 + 16 * NT + kReaders * kStaging);  // [E + 1]
+  int32_t* s_row = s_first + a.E + 1;                                    // row tiles before an expert; [E] its first row
+  int32_t* s_count = s_row + a.E;                                        // [E] its rows
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.w_stages; ++s) {
       mbar_init(w_full + 8 * s, 1);
-      mbar_init(w_empty + 8 * s, 8);           // two sets read a stage, a half each
+      mbar_init(w_empty + 8 * s, 4 * kStepsOfStage);  // a set of four warps reads what it makes a step of
     }
     for (int s = 0; s < kSteps; ++s) {
       mbar_init(x_full + 8 * s, 1);
@@ -394,17 +427,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     Part q;
     for (Walk at = start; ok && next_part(at, q);) {
       const int boxes = NT <= kBox ? 1 : (q.rows + kBox - 1) / kBox;
-      for (int i = 0; i < 2 * q.blocks; ++i, ++g, x.step(kSteps)) {
+      for (int i = 0; i < kStepsOfStage * q.blocks; ++i, ++g, x.step(kSteps)) {
         if (!warp_wait(step_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
           break;
         }
         if (elect_one()) {
-          mbar_expect_tx(x_full + 8 * x.slot, (uint32_t)(boxes * kBox * kXBlock * 2));
-          for (int c = 0; c < boxes; ++c)
-            tma_load_2d(x_ring + x.slot * kXStage + c * kBox * kXBlock * 2, &map_x, x_full + 8 * x.slot,
-                        (2 * q.k0 + i) * kXBlock, q.r0 + c * kBox, keep);
+          mbar_expect_tx(x_full + 8 * x.slot, (uint32_t)(kHalves * boxes * kBox * kXBlock * 2));
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            for (int c = 0; c < boxes; ++c)
+              tma_load_2d(x_ring + x.slot * kXStage + h * kXHalf + c * kBox * kXBlock * 2, &map_x, x_full + 8 * x.slot,
+                          (2 * q.k0 + kHalves * i + h) * kXBlock, q.r0 + c * kBox, keep);
         }
         __syncwarp();
       }
@@ -426,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t idesc = idesc_f16(kTileM, (q.rows + 15) & ~15);
       const uint32_t d = tmem + acc.slot * NT;
-      const int steps = 2 * q.blocks;
+      const int steps = kStepsOfStage * q.blocks;
       for (int i = 0; i < steps; ++i, step.step(kSteps)) {
         if (!warp_wait(step_full + 8 * step.slot, step.parity, abort_ptr, limit)) {
           if (lane == 0) give_up(kErrWaitFull);
@@ -435,11 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint64_t bdesc = smem_desc_sw128(x_ring + step.slot * kXStage);
-        const uint32_t w = tmem + kTmemA + step.slot * kAColumns;
+        const uint32_t w = tmem + kTmemA + step.slot * kStepColumns;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kXBlock / 16; ++kk)  // 16 FP16: 8 columns of A, 32 bytes along B's swizzled row
-            mma_f16_ts(d, w + 8 * kk, bdesc + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kHalves * kXBlock / 16; ++kk)  // 16 FP16: 8 columns of A, 32 bytes along B's swizzled row
+            mma_f16_ts(d, w + 8 * kk, bdesc + (kk / 4) * (kXHalf >> 4) + 2 * (kk % 4), idesc, (i > 0 || kk > 0) ? 1u : 0u);
           mma_commit(step_empty + 8 * step.slot);
           if (i == steps - 1) mma_commit(acc_full + 8 * acc.slot);
         }
@@ -452,43 +487,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kEpilogueWarps) {
     // ---------------- int8 to FP16, one TMEM lane a thread ----------------
-    // Set s takes the MMA steps s, s + kSets, ...: half s % 2 of every (kSets / 2)-th weight stage.
-    const int set = (warp - kEpilogueWarps) >> 2, half = set & 1, quarter = warp & 3;
-    const int row = quarter * 32 + lane;
+    // Set s takes the MMA steps s, s + kSets, ...: of a step that is half a weight stage, always the same half.
+    constexpr int kStride = kSets / kStepsOfStage;  // weight stages from one step of a set to its next
+    const int set = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane, first_half = kHalves == 1 ? set % 2 : 0;
     Ring w, step;
-    w.step(a.w_stages, set >> 1);
-    step.slot = set % kSteps;
-    step.parity = (uint32_t)(set / kSteps);
-    int ahead = set >> 1;  // weight stages until this set's next one
+    int ahead = set / kStepsOfStage;  // weight stages until this set's next one
+    w.step(a.w_stages, ahead);
+    step.slot = set;
     bool ok = true;
     Part q;
     for (Walk at = start; ok && next_part(at, q);) {
-      for (; ahead < q.blocks; ahead += kSets / 2, w.step(a.w_stages, kSets / 2), step.step(kSteps, kSets)) {
-        const int s = w.slot;
-        if (!warp_wait(w_full + 8 * s, w.parity, abort_ptr)) {
+      for (; ahead < q.blocks; ahead += kStride, w.step(a.w_stages, kStride), step.step(kSteps, kSets)) {
+        const uint32_t st = w_ring + w.slot * kWStage;
+        const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + step.slot * kStepColumns;
+        if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
           break;
         }
-        const uint32_t st = w_ring + s * kWStage;
-        uint32_t r[32];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint4 v = ld_shared_v4(st + sw128_offset(row, 4 * half + u));
-          int8x4_to_f16(v.x, r[8 * u], r[8 * u + 1]);
-          int8x4_to_f16(v.y, r[8 * u + 2], r[8 * u + 3]);
-          int8x4_to_f16(v.z, r[8 * u + 4], r[8 * u + 5]);
-          int8x4_to_f16(v.w, r[8 * u + 6], r[8 * u + 7]);
+        for (int h = 0; h < kHalves; ++h) {
+          uint32_t r[32];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 v = ld_shared_v4(st + sw128_offset(row, 4 * (first_half + h) + u));
+            int8x4_to_f16(v.x, r[8 * u], r[8 * u + 1]);
+            int8x4_to_f16(v.y, r[8 * u + 2], r[8 * u + 3]);
+            int8x4_to_f16(v.z, r[8 * u + 4], r[8 * u + 5]);
+            int8x4_to_f16(v.w, r[8 * u + 6], r[8 * u + 7]);
+          }
+          if (h == kHalves - 1) {  // all of it read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w_empty + 8 * w.slot);
+          }
+          if (h == 0) {
+            ok = warp_wait(step_empty + 8 * step.slot, step.parity ^ 1u, abort_ptr);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st32(dst + h * kAColumns, r);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(w_empty + 8 * s);
-        if (!warp_wait(step_empty + 8 * step.slot, step.parity ^ 1u, abort_ptr)) {
+        if (!ok) {
           if (lane == 0) give_up(kErrWaitEmpty);
-          ok = false;
           break;
         }
-        tc_fence_after();
-        tmem_st32(tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + step.slot * kAColumns, r);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         // one warp of the four sees the rows arrive too, so that the MMA warp has one barrier to wait for
         if (quarter == 0 && !warp_wait(x_full + 8 * step.slot, step.parity, abort_ptr)) {
@@ -503,51 +547,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- accumulators to BF16 ----------------
+    // A set of four warps reads every kReaders-th run of 16 columns, the next one on its way while one is written.
+    const int reader = warp >> 2, quarter = warp & 3;
     grid_dependency_wait();  // the counters
     Ring acc;
     bool ok = true;
     Part q;
     for (Walk at = start; ok && next_part(at, q); acc.step(kAccs)) {
       const int buf = acc.slot;
-      const int n = q.m0 + warp * 32 + lane;
+      const int n = q.m0 + quarter * 32 + lane;
       // the scales, while the MMAs run
       const float ws = n < a.N ? a.w_scale[(int64_t)q.e * a.N + n] : 0.0f;
-      for (int r = lane; r < NT; r += 32) s_scale[r] = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
+      for (int i = lane; i < NT / kReaders; i += 32) {
+        const int r = (i / kRun * kReaders + reader) * kRun + i % kRun;
+        s_scale[i] = r < q.rows ? a.x_scale[q.r0 + r] : 0.0f;
+      }
       __syncwarp();
       ok = warp_wait(acc_full + 8 * buf, acc.parity, abort_ptr);
       const bool whole = q.blocks == a.w_blocks;
-      if (!whole) ok = epilogue_all(ok);  // one answer for the warps that meet at barriers below
+      ok = all_of<32 * kEpilogueWarps>(ok);  // one answer for the warps that meet at barriers below
       if (!ok) {
         if (lane == 0) give_up(kErrWaitAccum);
         break;
       }
       tc_fence_after();
-      const uint32_t src = tmem + ((uint32_t)(warp * 32) << 16) + buf * NT;
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * NT;
       // FP32 sums [row][channel] of thread block c's part of a tile, this thread's channel
       auto sums = [&](int c, bool begins) {
-        return a.partial + (int64_t)(2 * c + (begins ? 1 : 0)) * NT * kTileM + warp * 32 + lane;
+        return a.partial + (int64_t)(2 * c + (begins ? 1 : 0)) * NT * kTileM + quarter * 32 + lane;
       };
       float* mine = sums(blockIdx.x, q.k0 == 0);
+      // Columns c .. c + 15 of the set's accumulator rows, scaled, to the result: by shared memory, so that a row's
+      // 128 channels leave as whole lines (two bytes a lane left 64 bytes at a time, and the tensor cores waited).
       auto finish16 = [&](const float (&v)[16], int c) {
-        if (n >= a.N) return;
-        uint16_t* out = a.out + (int64_t)(q.r0 + c) * a.N + n;
-        const int rows = q.rows - c;
+        const uint32_t mine16 = staging + 2 * (quarter * 32 + lane);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const uint4 s = ld_shared_v4(scale_addr + 4 * (c + i));
+          const uint4 s = ld_shared_v4(scales + 4 * (c / (kRun * kReaders) * kRun + i));
           const float sc[4] = {__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w)};
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
             const uint32_t two = bf16x2_pz(v[i + j] * ws * sc[j], v[i + j + 1] * ws * sc[j + 1]);
-            if (i + j < rows) out[(int64_t)(i + j) * a.N] = (uint16_t)two;
-            if (i + j + 1 < rows) out[(int64_t)(i + j + 1) * a.N] = (uint16_t)(two >> 16);
+            st_shared_u16(mine16 + (i + j) * (2 * kTileM), two);
+            st_shared_u16(mine16 + (i + j + 1) * (2 * kTileM), two >> 16);
           }
         }
+        set_bar(reader);
+        const int u = (quarter * 32 + lane) & 15;  // 8 channels of rows quarter * 2 + lane / 16 and 8 further
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * i + quarter * 2 + (lane >> 4);
+          const uint4 eight = ld_shared_v4(staging + r * (2 * kTileM) + 16 * u);
+          if (c + r < q.rows && q.m0 + 8 * u < a.N) st_v4(a.out + (int64_t)(q.r0 + c + r) * a.N + q.m0 + 8 * u, eight);
+        }
+        set_bar(reader);
       };
+      uint32_t next[16];
+      if (16 * reader < q.rows) tmem_ld16_begin(src + 16 * reader, next);
 #pragma unroll 1
-      for (int c = 0; c < q.rows; c += 16) {
+      for (int c = 16 * reader; c < q.rows; c += 16 * kReaders) {
         float v[16];
-        tmem_ld16(src + c, v);
+        tmem_ld16_end(next, v);
+        if (c + 16 * kReaders < q.rows) tmem_ld16_begin(src + c + 16 * kReaders, next);
         if (whole) {
           finish16(v, c);
         } else {
@@ -561,13 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) {
         const int first = owner(q.tile * a.w_blocks), last = owner((q.tile + 1) * a.w_blocks - 1);
         __threadfence();
-        epilogue_all(true);
+        all_of<32 * kEpilogueWarps>(true);
         if (threadIdx.x == 0) word[2] = atomicAdd(&a.counters[first], 1u);
-        epilogue_all(true);
+        all_of<32 * kEpilogueWarps>(true);
         if (word[2] == (unsigned)(last - first)) {  // the tile's last missing part: add them all, in order
           __threadfence();
 #pragma unroll 1
-          for (int c = 0; c < q.rows; c += 16) {
+          for (int c = 16 * reader; c < q.rows; c += 16 * kReaders) {
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -587,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             finish16(v, c);
           }
         }
-        epilogue_all(true);  // before word[2] is written again
+        all_of<32 * kEpilogueWarps>(true);  // before word[2] is written again
       }
     }
   }
@@ -623,8 +684,8 @@ Layout layout(int64_t R, int E, int D) {
 template <int NT>
 cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
   constexpr int kLimit = 227 * 1024;
-  constexpr int kXStage = NT * kXBlock * 2;
-  const int fixed = 1024 + 32 + 16 * NT + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
+  constexpr int kXStage = halves_of(NT) * NT * kXBlock * 2;
+  const int fixed = 1024 + 32 + 16 * NT + readers_of(NT) * kStaging + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
   constexpr int kSteps = steps_of(NT);
   a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
@@ -632,7 +693,7 @@ cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& 
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
   if (e != cudaSuccess) return e;
   const size_t smem = fixed + (size_t)kSteps * kXStage + (size_t)a.w_stages * kWStage;
-  return launch_pdl(kernel, dim3(sms < kMaxGrid ? sms : kMaxGrid), dim3(kThreads), smem, stream, map_w, map_x, a);
+  return launch_pdl(kernel, dim3(sms < kMaxGrid ? sms : kMaxGrid), dim3(threads_of(NT)), smem, stream, map_w, map_x, a);
 }
 
 }  // namespace
