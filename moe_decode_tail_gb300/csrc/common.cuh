@@ -45,6 +45,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2_pz(float lo, float hi) {
   return bf16_bits_pz(lo) | (bf16_bits_pz(hi) << 16);
 }
 
+// Two values in BF16 (nearest even), -0 made +0: the sum with +0 is exact but for that.
+__device__ __forceinline__ uint32_t bf16x2_pz(float lo, float hi) {
+  const __nv_bfloat162 v = __hadd2(__floats2bfloat162_rn(lo, hi), __floats2bfloat162_rn(0.0f, 0.0f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
   f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);

@@ -169,12 +169,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Two values in BF16 (nearest even), -0 made +0: the sum with +0 is exact but for that.
-__device__ __forceinline__ uint32_t bf16x2_pz(float lo, float hi) {
-  const __nv_bfloat162 v = __hadd2(__floats2bfloat162_rn(lo, hi), __floats2bfloat162_rn(0.0f, 0.0f));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Barrier 1 over `threads`; whether `ok` holds in all of them.
 template <int THREADS>
 __device__ __forceinline__ bool all_of(bool ok) {

@@ -58,6 +58,18 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int* all) {
   return sum - v + (warp > 0 ? before : 0);
 }
 
+// The lanes of the warp with this lane's value, by its bits: a ballot each (a match of 32 mostly different values
+// takes longer).
+__device__ __forceinline__ unsigned lanes_with(int value, int bits) {
+  unsigned same = 0xffffffffu;
+  for (int i = 0; i < bits; ++i) {
+    const bool one = (value >> i) & 1;
+    const unsigned ones = __ballot_sync(0xffffffffu, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
+}
+
 // Places of a chunk's routes.  A warp takes 32 * kSortPerLane consecutive routes, 32 at a time, so the order
 // within an expert is: earlier chunks, earlier warps, earlier rounds, lower lanes.
 __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortArgs a) {
@@ -70,6 +82,7 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
   __syncthreads();
   const int r0 = blockIdx.x * kSortChunk + warp * 32 * kSortPerLane + lane;
   int32_t* mine = s_mem + warp * a.E;
+  const int id_bits = 32 - __clz(a.E);
   int id[kSortPerLane], rank[kSortPerLane];
 #pragma unroll
   for (int j = 0; j < kSortPerLane; ++j) {
@@ -79,7 +92,7 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
   }
 #pragma unroll
   for (int j = 0; j < kSortPerLane; ++j) {
-    const unsigned same = __match_any_sync(0xffffffffu, id[j] < 0 ? -1 : id[j]);
+    const unsigned same = lanes_with(id[j] < 0 ? a.E : id[j], id_bits);
     const unsigned below = same & ((1u << lane) - 1u);
     rank[j] = 0;
     if (id[j] >= 0) rank[j] = mine[id[j]] + __popc(below);
@@ -213,8 +226,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
     }
   }
   if (v < nv)
-    st_v4(a.out + t * a.H + 8 * v, make_uint4(pack_bf16x2_pz(acc[0], acc[1]), pack_bf16x2_pz(acc[2], acc[3]),
-                                              pack_bf16x2_pz(acc[4], acc[5]), pack_bf16x2_pz(acc[6], acc[7])));
+    st_v4(a.out + t * a.H + 8 * v, make_uint4(bf16x2_pz(acc[0], acc[1]), bf16x2_pz(acc[2], acc[3]), bf16x2_pz(acc[4], acc[5]),
+                                              bf16x2_pz(acc[6], acc[7])));
 }
 
 // A block per token: d_out's row stays in registers while the routes' rows pass, the next route's loads in flight.
@@ -263,8 +276,8 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dot += f[e] * g[e];
         st_v4(a.d_rows + (int64_t)here * a.H + 8 * v,
-              make_uint4(pack_bf16x2_pz(w * g[0], w * g[1]), pack_bf16x2_pz(w * g[2], w * g[3]),
-                         pack_bf16x2_pz(w * g[4], w * g[5]), pack_bf16x2_pz(w * g[6], w * g[7])));
+              make_uint4(bf16x2_pz(w * g[0], w * g[1]), bf16x2_pz(w * g[2], w * g[3]), bf16x2_pz(w * g[4], w * g[5]),
+                         bf16x2_pz(w * g[6], w * g[7])));
       }
     }
 #pragma unroll

@@ -19,63 +19,70 @@ namespace moetail {
 
 namespace {
 
-// |v| as ordered bits: infinities are above every finite value and NaNs above them, so one unsigned maximum
-// finds the largest magnitude and whether anything was not finite.
+// The larger magnitude; a NaN stays one, so that a group's result tells whether all of it was finite.
+__device__ __forceinline__ float larger(float top, float v) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(top), "f"(fabsf(v)));
+  return m;
+}
+// The same of two results: as whole numbers, infinities are above every finite value and NaNs above them.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // What a group's largest magnitude gives: its scale, and the factors of the rounding.  Below 2^-100, M / top
 // could overflow, so the values are lifted by 2^100 first (exact); elsewhere that factor is 1.
 struct Rounding {
   float scale, lift, factor;
+  bool finite;
   __device__ Rounding(uint32_t top_bits, float most) {
     const float top = __uint_as_float(top_bits);
     lift = top < 0x1p-100f ? 0x1p100f : 1.0f;
     factor = top_bits == 0 ? 0.0f : most / (top * lift);
     scale = top / most;
-    if (top_bits >= 0x7f800000u) {
-      scale = __uint_as_float(0x7fffffffu);
-      factor = 0.0f;
-    }
+    finite = top_bits < 0x7f800000u;
+    if (!finite) scale = __uint_as_float(0x7fffffffu);
   }
 };
 
-// Eight values rounded to 8 bits.  A group that is not finite (scale NaN) gives zeros.
+// Four values, at most 127 (1 + 2^-22) in magnitude after the factor, as int8: the sum with 1.5 * 2^23 rounds to the
+// nearest even whole number, which stands in the low byte (one instruction, where a conversion takes several slots).
+__device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d, float factor) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t ia = __float_as_uint(__fmaf_rn(a, factor, kMagic)), ib = __float_as_uint(__fmaf_rn(b, factor, kMagic));
+  const uint32_t ic = __float_as_uint(__fmaf_rn(c, factor, kMagic)), id = __float_as_uint(__fmaf_rn(d, factor, kMagic));
+  return __byte_perm(__byte_perm(ia, ib, 0x0040), __byte_perm(ic, id, 0x0040), 0x5410);
+}
+
+// Eight values rounded to 8 bits; a group that is not finite gives zeros.
 template <int KIND>
 __device__ __forceinline__ uint2 round8(const float (&y)[8], const Rounding& r) {
-  const bool fine = r.scale == r.scale;
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fine ? (y[i] * r.lift) * r.factor : 0.0f;
+  for (int i = 0; i < 8; ++i) v[i] = y[i];
+  if (r.lift != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= r.lift;
+  }
   uint2 q;
   if (KIND == kQuantInt8) {
-    auto pack4 = [](float a, float b, float c, float d) {
-      // |v| is at most 127 (1 + 2^-22): it rounds to at most 127
-      uint32_t hi, all;
-      asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(__float2int_rn(d)), "r"(__float2int_rn(c)));
-      asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;"
-          : "=r"(all)
-          : "r"(__float2int_rn(b)), "r"(__float2int_rn(a)), "r"(hi));
-      return all;
-    };
-    q.x = pack4(v[0], v[1], v[2], v[3]);
-    q.y = pack4(v[4], v[5], v[6], v[7]);
+    q.x = int8x4(v[0], v[1], v[2], v[3], r.factor);
+    q.y = int8x4(v[4], v[5], v[6], v[7], r.factor);
   } else {
-    auto pair = [](float lo, float hi) {
-      return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    auto pair = [&](float lo, float hi) {
+      return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo * r.factor, hi * r.factor), __NV_SATFINITE, __NV_E4M3);
     };
     q.x = pair(v[0], v[1]) | (pair(v[2], v[3]) << 16);
     q.y = pair(v[4], v[5]) | (pair(v[6], v[7]) << 16);
   }
-  return q;
+  return r.finite ? q : make_uint2(0, 0);
 }
 
 constexpr float most_of(int kind) { return kind == kQuantInt8 ? 127.0f : 448.0f; }
 
 __device__ __forceinline__ uint32_t max8(const float (&y)[8]) {
-  uint32_t m = 0;
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, magnitude(y[i]));
-  return m;
+  for (int i = 0; i < 8; ++i) m = larger(m, y[i]);
+  return magnitude(m);
 }
 
 // Rows that this kernel may write in place: through L1 they would not be coherent, so no read-only loads.
@@ -140,9 +147,9 @@ __device__ __forceinline__ void store_rows(const float (&y)[VPT][8], uint32_t to
   }
 }
 
+// Eight values in BF16, -0 made +0.
 __device__ __forceinline__ uint4 pack8_pz(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2_pz(v[0], v[1]), pack_bf16x2_pz(v[2], v[3]), pack_bf16x2_pz(v[4], v[5]),
-                    pack_bf16x2_pz(v[6], v[7]));
+  return make_uint4(bf16x2_pz(v[0], v[1]), bf16x2_pz(v[2], v[3]), bf16x2_pz(v[4], v[5]), bf16x2_pz(v[6], v[7]));
 }
 
 // VPT: vectors of 8 columns of a thread; thread t holds vectors t, t + blockDim, ...  One reduction gives the sum
@@ -163,8 +170,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
       if (a.residual) res[i] = ld_rows(a.residual + row * a.H + 8 * v);
     }
   }
-  float h[VPT][8], sum = 0.0f;
-  uint32_t top = 0;
+  float h[VPT][8], sum = 0.0f, top = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
@@ -176,11 +182,11 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
     for (int e = 0; e < 8; ++e) {
       if (a.residual) h[i][e] += r[e];
       sum += h[i][e] * h[i][e];
-      if (!GROUPED) top = max(top, magnitude(h[i][e] * (g[e] + a.gain_center)));
+      if (!GROUPED) top = larger(top, h[i][e] * (g[e] + a.gain_center));
     }
     if (v < nv && a.residual_out) st_v4(a.residual_out + row * a.H + 8 * v, pack8_pz(h[i]));
   }
-  const RowSums sums = block_reduce(sum, top);
+  const RowSums sums = block_reduce(sum, magnitude(top));
   const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sums.sum * a.rcpH + a.eps));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
