@@ -61,7 +61,7 @@ cudaError_t launch_silu_quant(const SiluQuantArgs& a, int kind, bool grouped, in
 
 // ---- routes (routes.cu) ----------------------------------------------------------
 
-constexpr int kSortChunk = 4096;  // routes of one thread block
+int sort_blocks(int routes);  // thread blocks of a sort, each with a row of counts in the workspace
 
 struct SortArgs {
   const int32_t* ids;     // [routes]

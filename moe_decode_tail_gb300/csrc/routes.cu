@@ -14,18 +14,19 @@ namespace moetail {
 
 namespace {
 
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortPerLane = kSortChunk / kSortThreads;
+constexpr int kSortThreads = 1024, kSortWarps = 32;
 
-// Routes of each expert in every chunk of kSortChunk routes.
+// Routes of each expert in every chunk of PER * 1024 routes.
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) count_routes_kernel(const SortArgs a) {
   extern __shared__ int32_t s_count[];
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) s_count[e] = 0;
   grid_dependency_wait();
   launch_dependents();
   __syncthreads();
-  const int r0 = blockIdx.x * kSortChunk;
+  const int r0 = blockIdx.x * PER * kSortThreads;
 #pragma unroll
-  for (int j = 0; j < kSortPerLane; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const int r = r0 + j * kSortThreads + threadIdx.x;
     const int e = r < a.routes ? a.ids[r] : -1;
     if (e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);  // whole numbers: the order does not matter
@@ -70,28 +71,31 @@ __device__ __forceinline__ unsigned lanes_with(int value, int bits) {
   return same;
 }
 
-// Places of a chunk's routes.  A warp takes 32 * kSortPerLane consecutive routes, 32 at a time, so the order
+// Places of a chunk's routes.  A warp takes 32 * PER consecutive routes, 32 at a time, so the order
 // within an expert is: earlier chunks, earlier warps, earlier rounds, lower lanes.
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortArgs a) {
-  extern __shared__ int32_t s_mem[];  // [warps][E] counts, then the routes of the warps before; [E] first place
-  int32_t* s_first = s_mem + kSortWarps * a.E;
+  // [warps][E] counts, then the routes of the warps before; [E] first place; [E], [E] routes of all chunks, of those
+  // before this one
+  extern __shared__ int32_t s_mem[];
+  int32_t *s_first = s_mem + kSortWarps * a.E, *s_total = s_first + a.E, *s_before = s_total + a.E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * a.E; i += kSortThreads) s_mem[i] = 0;
+  for (int i = threadIdx.x; i < (kSortWarps + 3) * a.E; i += kSortThreads) s_mem[i] = 0;
   grid_dependency_wait();
   launch_dependents();
   __syncthreads();
-  const int r0 = blockIdx.x * kSortChunk + warp * 32 * kSortPerLane + lane;
+  const int r0 = (blockIdx.x * kSortThreads + warp * 32) * PER + lane;
   int32_t* mine = s_mem + warp * a.E;
   const int id_bits = 32 - __clz(a.E);
-  int id[kSortPerLane], rank[kSortPerLane];
+  int id[PER], rank[PER];
 #pragma unroll
-  for (int j = 0; j < kSortPerLane; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const int r = r0 + 32 * j;
     id[j] = r < a.routes ? a.ids[r] : -1;
     if (id[j] >= a.E) id[j] = -1;
   }
 #pragma unroll
-  for (int j = 0; j < kSortPerLane; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const unsigned same = lanes_with(id[j] < 0 ? a.E : id[j], id_bits);
     const unsigned below = same & ((1u << lane) - 1u);
     rank[j] = 0;
@@ -99,6 +103,20 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
     __syncwarp();
     if (id[j] >= 0 && below == 0) mine[id[j]] += __popc(same);
     __syncwarp();
+  }
+  if (gridDim.x > 1) {  // every thread takes an expert's counts of some chunks
+    const int groups = kSortThreads / a.E, e = threadIdx.x % a.E, g = threadIdx.x / a.E;
+    if (g < groups) {
+      int total = 0, before = 0;
+#pragma unroll 4
+      for (int c = g; c < (int)gridDim.x; c += groups) {
+        const int n = a.counts[(int64_t)c * a.E + e];
+        if (c < (int)blockIdx.x) before += n;
+        total += n;
+      }
+      atomicAdd(&s_total[e], total);  // whole numbers: the order does not matter
+      atomicAdd(&s_before[e], before);
+    }
   }
   __syncthreads();
   const int e = threadIdx.x;  // E <= 1024
@@ -111,13 +129,8 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
       total += n;
     }
     if (gridDim.x > 1) {
-      total = 0;
-#pragma unroll 8
-      for (int c = 0; c < (int)gridDim.x; ++c) {
-        const int n = a.counts[(int64_t)c * a.E + e];
-        if (c < (int)blockIdx.x) before += n;
-        total += n;
-      }
+      total = s_total[e];
+      before = s_before[e];
     }
   }
   int all;
@@ -129,7 +142,7 @@ __global__ void __launch_bounds__(kSortThreads) place_routes_kernel(const SortAr
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kSortPerLane; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const int r = r0 + 32 * j;
     if (r >= a.routes) continue;
     int place = -1;
@@ -294,16 +307,37 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(const CombineArgs a)
 
 }  // namespace
 
-cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t stream) {
-  const int blocks = a.routes > kSortChunk ? (a.routes + kSortChunk - 1) / kSortChunk : 1;
-  const size_t smem = (size_t)(kSortWarps + 1) * a.E * 4;
-  cudaError_t e = ensure_smem_limit((const void*)place_routes_kernel, (kSortWarps + 1) * kMaxExperts * 4);
+namespace {
+
+template <int PER>
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
+  const int blocks = sort_blocks(a.routes);
+  cudaError_t e = ensure_smem_limit((const void*)place_routes_kernel<PER>, (kSortWarps + 3) * kMaxExperts * 4);
   if (e != cudaSuccess) return e;
   if (blocks > 1) {
-    e = launch_pdl(count_routes_kernel, dim3(blocks), dim3(kSortThreads), (size_t)a.E * 4, stream, a);
+    e = launch_pdl(count_routes_kernel<PER>, dim3(blocks), dim3(kSortThreads), (size_t)a.E * 4, stream, a);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(place_routes_kernel, dim3(blocks), dim3(kSortThreads), smem, stream, a);
+  return launch_pdl(place_routes_kernel<PER>, dim3(blocks), dim3(kSortThreads), (size_t)(kSortWarps + 3) * a.E * 4, stream,
+                    a);
+}
+
+// Routes of a lane: few, until there would be more than 128 chunks (each thread block adds up the counts of all).
+int routes_of_lane(int routes) { return routes <= 128 * 1024 ? 1 : routes <= 4 * 128 * 1024 ? 4 : 16; }
+
+}  // namespace
+
+int sort_blocks(int routes) {
+  const int chunk = kSortThreads * routes_of_lane(routes);
+  return routes > chunk ? (routes + chunk - 1) / chunk : 1;
+}
+
+cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t stream) {
+  switch (routes_of_lane(a.routes)) {
+    case 1: return launch_sort<1>(a, stream);
+    case 4: return launch_sort<4>(a, stream);
+    default: return launch_sort<16>(a, stream);
+  }
 }
 
 cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t stream) {
