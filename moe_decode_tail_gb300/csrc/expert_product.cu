@@ -109,6 +109,10 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint1
   }
 }
 
+// Brings the warp's lanes together: before instructions that all of them have to execute at once (".aligned"), which
+// the compiler does not know of inside inline assembly and might place in the branches before them.
+__device__ __forceinline__ void together() { __syncwarp(); }
+
 // ---- PTX of this kernel -------------------------------------------------------------
 
 // D[tmem_d] (+)= A[tmem_a] * B[bdesc], FP16 operands, FP32 sums.
@@ -127,6 +131,7 @@ __device__ __forceinline__ uint32_t idesc_f16(int m, int n) {
 }
 // 32 consecutive TMEM columns of this thread's lane (to be waited for).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  together();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -137,29 +142,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-// 16 consecutive accumulator columns of this thread's lane: asked for, and there.
-__device__ __forceinline__ void tmem_ld16_begin(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16_end(uint32_t (&r)[16], float (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+__device__ __forceinline__ void tmem_st_wait() {
+  together();
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 // A barrier over the four warps of an epilogue set.
-__device__ __forceinline__ void set_bar(int set) { asm volatile("bar.sync %0, 128;" ::"r"(2 + set) : "memory"); }
+__device__ __forceinline__ void set_bar(int set) {
+  together();
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + set) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             uint64_t policy) {
   asm volatile(
@@ -173,6 +167,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 template <int THREADS>
 __device__ __forceinline__ bool all_of(bool ok) {
   uint32_t all;
+  together();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -526,7 +521,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
           if (lane == 0) give_up(kErrWaitEmpty);
           break;
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tmem_st_wait();
         tc_fence_before();
         // one warp of the four sees the rows arrive too, so that the MMA warp has one barrier to wait for
         if (quarter == 0 && !warp_wait(x_full + 8 * step.slot, step.parity, abort_ptr)) {
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     }
   } else {
     // ---------------- accumulators to BF16 ----------------
-    // A set of four warps reads every kReaders-th run of 16 columns, the next one on its way while one is written.
+    // A set of four warps reads every kReaders-th run of 16 columns.
     const int reader = warp >> 2, quarter = warp & 3;
     grid_dependency_wait();  // the counters
     Ring acc;
@@ -596,13 +591,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         }
         set_bar(reader);
       };
-      uint32_t next[16];
-      if (16 * reader < q.rows) tmem_ld16_begin(src + 16 * reader, next);
 #pragma unroll 1
       for (int c = 16 * reader; c < q.rows; c += 16 * kReaders) {
         float v[16];
-        tmem_ld16_end(next, v);
-        if (c + 16 * kReaders < q.rows) tmem_ld16_begin(src + c + 16 * kReaders, next);
+        together();
+        tmem_ld16(src + c, v);
         if (whole) {
           finish16(v, c);
         } else {
@@ -683,6 +676,11 @@ cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& 
   constexpr int kSteps = steps_of(NT);
   a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
+  // A set of converting warps that takes every second stage must meet the same slots in every round: else it could ask
+  // for a slot's next round while the other set's copy in it is still on its way, and the parity of the round before
+  // would tell it that its own had landed.
+  constexpr int kStride = kSets * halves_of(NT) / 2;
+  a.w_stages -= a.w_stages % kStride;
   auto kernel = expert_product_kernel<NT>;
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
   if (e != cudaSuccess) return e;
@@ -714,8 +712,10 @@ cudaError_t launch_expert_product(const ProductArgs& p, const CUtensorMap& map_w
   a.stage_wait_ns = stage_wait_limit_ns();
   const int64_t vectors = p.R * p.D / 16;
   const int64_t blocks = (vectors + 256 * kExpand - 1) / (256 * kExpand);
-  cudaError_t e = launch_pdl(expand_rows_kernel, dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, stream,
-                             p.x, reinterpret_cast<uint16_t*>(ws + l.x16), p.offsets, p.E, p.R, p.D, a.counters);
+  // at most as many blocks as run at once, so that none is left to start when the product's blocks take the SMs
+  const int most = 5 * sms;
+  cudaError_t e = launch_pdl(expand_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, stream, p.x,
+                             reinterpret_cast<uint16_t*>(ws + l.x16), p.offsets, p.E, p.R, p.D, a.counters);
   if (e != cudaSuccess) return e;
   switch (rows_of_tile(p.R, p.E)) {
     case 16: return launch_nt<16>(map_w, map_x, a, sms, stream);

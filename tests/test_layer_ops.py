@@ -412,6 +412,54 @@ def test_expert_product(E, N, D):
         check_product(product(x, xs, w, ws, offsets), x, xs, w, ws, offsets)
 
 
+@pytest.mark.parametrize("b", [4, 100, 200, 500, 1000, 3000])
+def test_expert_product_over_many_tiles(b):
+    # several tiles for every thread block at each tile height (16 to 256 rows), uneven experts with several row tiles,
+    # the reduction longer than the rings; several calls in flight at once, each reading what the last one left
+    g = gen(b)
+    E, K, N, D = 64, 4, 1032, 2064
+    w, ws = int8(g, E, N, D), scales(g, E, N)
+    ids = (torch.rand((b, E), generator=g, device="cuda") * torch.linspace(1.0, 3.0, E, device="cuda")).topk(K, 1).indices
+    offsets, _, _ = plain_sort(ids.to(I32), E)
+    R = b * K
+    x, xs = int8(g, R, D), scales(g, R)
+    out = product(x, xs, w, ws, offsets)
+    work = torch.empty(mt.moe_tail_expert_product_workspace_bytes(R, E, N, D), dtype=torch.uint8, device="cuda")
+    again = [filled(BF, R, N) for _ in range(6)]
+    for o in again:
+        mt.moe_tail_expert_product(x, xs, w, ws, o, work, expert_offsets=offsets)
+    check_product(out, x, xs, w, ws, offsets)
+    assert all(torch.equal(o, out) for o in again)
+    assert mt.moe_tail_take_device_error() == 0
+
+
+@pytest.mark.parametrize("b", [512, 1024])
+def test_expert_product_of_a_weight_that_streams(b):
+    # 1 GB of weights, so that copies land late and in any order, at 64 and 128 rows a tile
+    g = gen(b)
+    E, K, N, D = 128, 8, 2048, 4096
+    w, ws = int8(g, E, N, D // 4).repeat(1, 1, 4), scales(g, E, N)
+    ids = (torch.rand((b, E), generator=g, device="cuda") * torch.linspace(1.0, 2.0, E, device="cuda")).topk(K, 1).indices
+    offsets, _, _ = plain_sort(ids.to(I32), E)
+    x, xs = int8(g, b * K, D), scales(g, b * K)
+    out = product(x, xs, w, ws, offsets)
+    check_product(out, x, xs, w, ws, offsets)
+    work = torch.empty(mt.moe_tail_expert_product_workspace_bytes(b * K, E, N, D), dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        again = filled(BF, b * K, N)
+        mt.moe_tail_expert_product(x, xs, w, ws, again, work, expert_offsets=offsets)
+        assert torch.equal(again, out)
+    assert mt.moe_tail_take_device_error() == 0
+
+
+@pytest.mark.parametrize("R", [80, 128])
+def test_dense_product_of_tall_tiles(R):
+    g = gen(R)
+    N, D = 19456 // 2, 2000
+    w, ws, x, xs = int8(g, 1, N, D), scales(g, 1, N), int8(g, R, D), scales(g, R)
+    check_product(product(x, xs, w, ws, None), x, xs, w, ws, None)
+
+
 def test_product_at_the_largest_sums_and_with_scales_that_are_not_finite():
     g = gen(3)
     R, N, D = 40, 256, 4096
@@ -439,6 +487,24 @@ def test_product_with_offsets_that_are_no_partition():
                                    expert_offsets=torch.tensor(bad, dtype=I32, device="cuda"))
         torch.cuda.synchronize()
         assert (big[:32] == 77).all() and (big[32 + R:] == 77).all()
+    assert mt.moe_tail_take_device_error() == 0
+
+
+def test_product_whose_waits_run_out():
+    # a limit of one nanosecond on the tensor cores' operands: the call gives up, says so and leaves the device usable
+    g = gen(8)
+    E, N, D, R = 4, 256, 512, 60
+    w, ws, x, xs = int8(g, E, N, D), scales(g, E, N), int8(g, R, D), scales(g, R)
+    offsets = torch.tensor([0, 20, 20, 45, 60], dtype=I32, device="cuda")
+    assert mt.moe_tail_take_device_error() == 0
+    mt.moe_tail_set_stage_wait_limit(1)
+    try:
+        product(x, xs, w, ws, offsets)
+        torch.cuda.synchronize()
+    finally:
+        mt.moe_tail_set_stage_wait_limit(0)
+    assert mt.moe_tail_take_device_error() & 1
+    check_product(product(x, xs, w, ws, offsets), x, xs, w, ws, offsets)
     assert mt.moe_tail_take_device_error() == 0
 
 
