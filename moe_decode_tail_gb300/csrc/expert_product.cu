@@ -270,23 +270,26 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   int32_t* s_row = s_first + a.E + 1;                                    // row tiles before an expert; [E] its first row
   int32_t* s_count = s_row + a.E;                                        // [E] its rows
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < a.w_stages; ++s) {
+  if (warp == 0) {
+    for (int s = lane; s < a.w_stages; s += 32) {
       mbar_init(w_full + 8 * s, 1);
       mbar_init(w_empty + 8 * s, 4 * kStepsOfStage);  // a set of four warps reads what it makes a step of
     }
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = lane; s < kSteps; s += 32) {
       mbar_init(x_full + 8 * s, 1);
       mbar_init(step_full + 8 * s, 4);
       mbar_init(step_empty + 8 * s, 1);
     }
-    for (int s = 0; s < kAccs; ++s) {
-      mbar_init(acc_full + 8 * s, 1);
-      mbar_init(acc_empty + 8 * s, kEpilogueWarps);
+    if (lane < kAccs) {
+      mbar_init(acc_full + 8 * lane, 1);
+      mbar_init(acc_empty + 8 * lane, kEpilogueWarps);
     }
-    mbar_init(mma_done, 1);
-    *abort_ptr = 0;
+    if (lane == 0) {
+      mbar_init(mma_done, 1);
+      *abort_ptr = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kWarpW && lane == 0) {
     prefetch_map(&map_w);
     prefetch_map(&map_x);
   }
@@ -506,10 +509,6 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
             int8x4_to_f16(v.z, r[8 * u + 4], r[8 * u + 5]);
             int8x4_to_f16(v.w, r[8 * u + 6], r[8 * u + 7]);
           }
-          if (h == kHalves - 1) {  // all of it read
-            __syncwarp();
-            if (lane == 0) mbar_arrive(w_empty + 8 * w.slot);
-          }
           if (h == 0) {
             ok = warp_wait(step_empty + 8 * step.slot, step.parity ^ 1u, abort_ptr);
             if (!ok) break;
@@ -523,6 +522,9 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         }
         tmem_st_wait();
         tc_fence_before();
+        __syncwarp();
+        // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
+        if (lane == 0) mbar_arrive(w_empty + 8 * w.slot);
         // one warp of the four sees the rows arrive too, so that the MMA warp has one barrier to wait for
         if (quarter == 0 && !warp_wait(x_full + 8 * step.slot, step.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
@@ -561,11 +563,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
       }
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * NT;
-      // FP32 sums [row][channel] of thread block c's part of a tile, this thread's channel
-      auto sums = [&](int c, bool begins) {
-        return a.partial + (int64_t)(2 * c + (begins ? 1 : 0)) * NT * kTileM + quarter * 32 + lane;
-      };
-      float* mine = sums(blockIdx.x, q.k0 == 0);
+      // FP32 sums [row][channel] of this thread block's part of a tile, this thread's channel
+      float* mine = a.partial + (int64_t)(2 * blockIdx.x + (q.k0 == 0 ? 1 : 0)) * NT * kTileM + quarter * 32 + lane;
       // Columns c .. c + 15 of the set's accumulator rows, scaled, to the result: by shared memory, so that a row's
       // 128 channels leave as whole lines (two bytes a lane left 64 bytes at a time, and the tensor cores waited).
       auto finish16 = [&](const float (&v)[16], int c) {
@@ -614,25 +613,47 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         all_of<32 * kEpilogueWarps>(true);
         if (word[2] == (unsigned)(last - first)) {  // the tile's last missing part: add them all, in order
           __threadfence();
+          // a warp takes four rows of each run, a lane four channels: four parts' loads in flight
+          const int n4 = q.m0 + 4 * lane;
+          const float* w4 = a.w_scale + (int64_t)q.e * a.N + n4;
+          float wsc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) wsc[i] = n4 < a.N ? w4[i] : 0.0f;
+          const float* sums0 = a.partial + quarter * 4 * kTileM + 4 * lane;
 #pragma unroll 1
-          for (int c = 16 * reader; c < q.rows; c += 16 * kReaders) {
-            float v[16];
+          for (int c = kRun * reader; c < q.rows; c += kRun * kReaders) {
+            float4 v[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            for (int s = first; s <= last; s += 2) {  // two parts' loads in flight
-              float u[2][16];
+            for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = first; s <= last; s += 4) {
+              float4 u[4][4];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float* theirs = sums(min(s + k, last), s + k == first) + c * kTileM;
+              for (int k = 0; k < 4; ++k) {
+                const float* theirs = sums0 + (int64_t)(2 * (s + k) + (s + k == first ? 1 : 0)) * NT * kTileM + c * kTileM;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[k][i] = s + k <= last ? __ldcg(theirs + i * kTileM) : 0.0f;
+                for (int j = 0; j < 4; ++j)
+                  u[k][j] = s + k <= last ? __ldcg(reinterpret_cast<const float4*>(theirs + j * kTileM))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
               }
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
+              for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += u[k][i];
+                for (int j = 0; j < 4; ++j) {
+                  v[j].x += u[k][j].x;
+                  v[j].y += u[k][j].y;
+                  v[j].z += u[k][j].z;
+                  v[j].w += u[k][j].w;
+                }
             }
-            finish16(v, c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int row = c + quarter * 4 + j;
+              if (row >= q.rows || n4 >= a.N) continue;
+              const float xs = a.x_scale[q.r0 + row];
+              const uint2 four = make_uint2(bf16x2_pz(v[j].x * wsc[0] * xs, v[j].y * wsc[1] * xs),
+                                            bf16x2_pz(v[j].z * wsc[2] * xs, v[j].w * wsc[3] * xs));
+              *reinterpret_cast<uint2*>(a.out + (int64_t)(q.r0 + row) * a.N + n4) = four;
+            }
           }
         }
         all_of<32 * kEpilogueWarps>(true);  // before word[2] is written again
