@@ -389,8 +389,9 @@ int moe_tail_take_device_error(unsigned int* bits);
 int moe_tail_selftest_wait_timeout(unsigned int limit_us, void* stream);
 
 /* Failure-detection test hook (no counterpart on the pages): the limit of
- * the operand-stage waits -- the GEMM kernels' tensor-core issuer waiting for
- * a stage of weights and tokens, the staged expert-TP finalize kernel's
+ * the operand-stage waits -- the tensor-core issuer of the GEMM kernels and
+ * of the 8-bit product waiting for a stage of weights and tokens, the staged
+ * expert-TP finalize kernel's
  * threads waiting for a stage of route rows -- for calls made after it
  * returns (process-wide), in nanoseconds (1: give up at the first such
  * wait, whether or not the stage has landed); 0 restores the default (0.5 s).

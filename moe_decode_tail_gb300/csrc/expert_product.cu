@@ -13,8 +13,13 @@
 //            of its rows (its N).  The weight bytes arrive by TMA (128 channels x 128 bytes a stage); eight warps
 //            turn them into FP16 in registers and store them into tensor memory, from where the MMA takes its A
 //            operand (a thread's row is a TMEM lane, so nothing is shuffled or written back to shared memory);
-//            the FP16 rows arrive by TMA as the B operand; four warps read finished accumulators, scale them and
-//            write BF16.  Warp roles meet at mbarriers only, so the weight stream runs on across tiles.
+//            the FP16 rows arrive by TMA as the B operand; four warps (eight at 256 rows) read finished
+//            accumulators, scale them and write BF16.  The weight stream runs on across tiles.
+//
+// With few rows for an expert the weights' way from memory is the bound: 64 tokens x 8 routes over 128 experts of
+// 2048 x 4096 take 175 us (1.06 GB, 0.90 of the measured copy rate; the product kernel alone 157 us, all of it).
+// With many, the tensor cores and what feeds them: 8192 rows by 8192 channels x 4096 in 353 us, 1.56 PFLOP/s (0.84
+// of a library BF16 product); 32768 rows over the 128 experts in 500 us, of which expand takes 75.
 //
 // The tiles that are no multiple of the thread blocks (with few rows, all of them) are dealt out by reduction
 // blocks, the same number to each thread block, so such a tile may begin in one and end in another.  A part's FP32
@@ -42,7 +47,7 @@ constexpr int kWBlock = 128;                   // reduction bytes of a weight st
 constexpr int kWStage = kTileM * kWBlock;      // 16 KB
 constexpr int kXBlock = 64;                    // FP16 of a row stage: one swizzle row
 constexpr int kAColumns = kXBlock / 2;         // TMEM columns of a weight half stage: two FP16 each
-constexpr int kSets = 2;                       // sets of four converting warps, a warp for each TMEM quarter
+constexpr int kSets = 2;                       // sets of four converting warps, a warp for each TMEM quarter (four: no faster)
 constexpr int kMaxGrid = 160;                  // thread blocks: each has at most two parts of a tile
 constexpr int kLeastBlocks = 4;                // reduction blocks a thread block is worth
 
@@ -184,7 +189,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   if (limit_ns > 1 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, abort_flag));
 }
-// True in one lane of a converged warp.
+// True in one lane of a converged warp.  The issuing warps walk their loops whole and issue under it: with one lane in
+// the loop every operand of a copy or an MMA went from vector to uniform registers first (411 -> 211 us in decode).
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -220,7 +226,8 @@ struct Part {
 
 // NT: rows of a tile (the accumulator's columns).
 // A step of the MMA warp takes `halves` of a weight stage, 64 of the reduction each: what a step costs besides its
-// MMAs (a wait, a commit) is then paid half as often.  With 256 rows shared memory has no room for two.
+// MMAs (a wait, a commit) is then paid half as often (decode: 180 us, 200 with one).  With 256 rows shared memory has
+// no room for two.
 constexpr int halves_of(int nt) { return nt > 128 ? 1 : 2; }
 // Steps in flight: what tensor memory has beside the accumulators; with 256 rows shared memory is the limit.
 constexpr int steps_of(int nt) { return nt > 128 ? 5 : (512 - 2 * nt) / (2 * kAColumns); }
@@ -329,7 +336,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   // [my_begin, my_end) of them to this thread block; then come whole tiles, one in gridDim.x.
   const int64_t tiles = (int64_t)s_first[a.E] * m_tiles;
   // Dealing saves the idle part of a last wave, w_blocks * (1 - odd / grid) reduction blocks, and costs the FP32
-  // sums' way through memory: about one reduction block's time for 16 rows.
+  // sums' way through memory: about one reduction block's time for 16 rows (16 rows, 2016 tiles: 206 -> 200 us; 256
+  // rows, about 3000 tiles: 735 us without it, 807 with it).
   const int odd = (int)(tiles % gridDim.x);
   const int64_t dealt = (int64_t)a.w_blocks * (gridDim.x - odd) > (int64_t)(NT / 16) * gridDim.x ? odd : 0;
   const int64_t total = dealt * a.w_blocks;
@@ -669,7 +677,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
 // ---- host ----------------------------------------------------------------------------
 
 // Rows of a tile: all of them where one expert has few, else twice an expert's average share, so that an uneven
-// batch still has one row tile for most experts.
+// batch still has one row tile for most experts.  (128 experts, 32 rows each on average: 200 us with tiles of 64,
+// 243 with tiles of 256; at 256 each, 500 us with 256.)
 int rows_of_tile(int64_t R, int E) {
   const int64_t want = E == 1 ? R : 2 * ((R + E - 1) / E);
   return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
