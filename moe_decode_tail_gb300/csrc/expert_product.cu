@@ -224,6 +224,11 @@ struct Part {
   bool shared;  // more than one row tile reads this expert's weights
 };
 
+// A tile whose parts are all in the workspace, by the thread blocks first .. last.
+struct Split {
+  int e, m0, r0, rows, first, last;
+};
+
 // NT: rows of a tile (the accumulator's columns).
 // A step of the MMA warp takes `halves` of a weight stage, 64 of the reduction each: what a step costs besides its
 // MMAs (a wait, a commit) is then paid half as often (decode: 180 us, 200 with one).  With 256 rows shared memory has
@@ -267,8 +272,12 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   const uint32_t x_full = bars(kSteps), step_full = bars(kSteps), step_empty = bars(kSteps);
   const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
   at = (at + 15u) & ~15u;
-  volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort, last part
+  // TMEM base, abort, parts finished before this one, tiles in s_split
+  volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));
   volatile uint32_t* abort_ptr = word + 1;
+  const uint32_t slot = at;
+  Split* s_split = reinterpret_cast<Split*>(base_ptr + (at - base) + 16);  // [2] that this thread block is to add up
+  at += 64;
   // an epilogue warp's scales of the rows it writes [NT / kReaders], and its set's BF16 [kRun][128]
   const uint32_t scales = at + 16 + (warp % kEpilogueWarps) * (NT / kReaders) * 4;
   float* s_scale = reinterpret_cast<float*>(base_ptr + (scales - base));
@@ -294,13 +303,14 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     if (lane == 0) {
       mbar_init(mma_done, 1);
       *abort_ptr = 0;
+      word[3] = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (warp == kWarpW && lane == 0) {
     prefetch_map(&map_w);
     prefetch_map(&map_x);
   }
-  if (warp == kWarpMma) tmem_alloc(at, 512);
+  if (warp == kWarpMma) tmem_alloc(slot, 512);
   // The experts' rows and row tiles.  The offsets were complete before the expand kernel let this one start.
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     const int begin = a.offsets ? clamp_row(a.offsets[e], a.R) : 0;
@@ -383,6 +393,50 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     q.tile = tile;
     q.shared = row_tiles > 1;
     return true;
+  };
+  // The parts of a tile added up in the order of the reduction, scaled and written by warp w of `warps`: four rows at a
+  // time, four channels a lane, four parts' loads in flight.
+  auto add_parts = [&](const Split& q, int w, int warps) {
+    const int n4 = q.m0 + 4 * lane;
+    const float* scale4 = a.w_scale + (int64_t)q.e * a.N + n4;
+    float ws[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ws[i] = n4 < a.N ? scale4[i] : 0.0f;
+#pragma unroll 1
+    for (int r = 4 * w; r < q.rows; r += 4 * warps) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = q.first; s <= q.last; s += 4) {
+        float4 u[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float* sums =
+              a.partial + ((int64_t)(2 * (s + k) + (s + k == q.first ? 1 : 0)) * NT + r) * kTileM + 4 * lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            u[k][j] = s + k <= q.last ? __ldcg(reinterpret_cast<const float4*>(sums + j * kTileM))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j].x += u[k][j].x;
+            v[j].y += u[k][j].y;
+            v[j].z += u[k][j].z;
+            v[j].w += u[k][j].w;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r + j >= q.rows || n4 >= a.N) continue;
+        const float xs = a.x_scale[q.r0 + r + j];
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(q.r0 + r + j) * a.N + n4) =
+            make_uint2(bf16x2_pz(v[j].x * ws[0] * xs, v[j].y * ws[1] * xs),
+                       bf16x2_pz(v[j].z * ws[2] * xs, v[j].w * ws[3] * xs));
+      }
+    }
   };
   auto give_up = [&](unsigned bit) {
     if (!*abort_ptr) raise_error(bit);
@@ -621,48 +675,9 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         all_of<32 * kEpilogueWarps>(true);
         if (word[2] == (unsigned)(last - first)) {  // the tile's last missing part: add them all, in order
           __threadfence();
-          // a warp takes four rows of each run, a lane four channels: four parts' loads in flight
-          const int n4 = q.m0 + 4 * lane;
-          const float* w4 = a.w_scale + (int64_t)q.e * a.N + n4;
-          float wsc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) wsc[i] = n4 < a.N ? w4[i] : 0.0f;
-          const float* sums0 = a.partial + quarter * 4 * kTileM + 4 * lane;
-#pragma unroll 1
-          for (int c = kRun * reader; c < q.rows; c += kRun * kReaders) {
-            float4 v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s = first; s <= last; s += 4) {
-              float4 u[4][4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float* theirs = sums0 + (int64_t)(2 * (s + k) + (s + k == first ? 1 : 0)) * NT * kTileM + c * kTileM;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  u[k][j] = s + k <= last ? __ldcg(reinterpret_cast<const float4*>(theirs + j * kTileM))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  v[j].x += u[k][j].x;
-                  v[j].y += u[k][j].y;
-                  v[j].z += u[k][j].z;
-                  v[j].w += u[k][j].w;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int row = c + quarter * 4 + j;
-              if (row >= q.rows || n4 >= a.N) continue;
-              const float xs = a.x_scale[q.r0 + row];
-              const uint2 four = make_uint2(bf16x2_pz(v[j].x * wsc[0] * xs, v[j].y * wsc[1] * xs),
-                                            bf16x2_pz(v[j].z * wsc[2] * xs, v[j].w * wsc[3] * xs));
-              *reinterpret_cast<uint2*>(a.out + (int64_t)(q.r0 + row) * a.N + n4) = four;
-            }
-          }
+          const Split tile = {q.e, q.m0, q.r0, q.rows, first, last};
+          if (tiles >= gridDim.x) add_parts(tile, warp, kEpilogueWarps);  // whole tiles follow: their MMAs go on meanwhile
+          else if (threadIdx.x == 0) s_split[word[3]++] = tile;           // nothing does: every warp helps, at the end
         }
         all_of<32 * kEpilogueWarps>(true);  // before word[2] is written again
       }
@@ -672,6 +687,10 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (!*abort_ptr) {
+    __threadfence();
+    for (unsigned i = 0; i < word[3]; ++i) add_parts(s_split[i], warp, kThreads / 32);
+  }
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -702,7 +721,7 @@ template <int NT>
 cudaError_t launch_nt(const CUtensorMap& map_w, const CUtensorMap& map_x, Args& a, int sms, cudaStream_t stream) {
   constexpr int kLimit = 227 * 1024;
   constexpr int kXStage = halves_of(NT) * NT * kXBlock * 2;
-  const int fixed = 1024 + 32 + 16 * NT + readers_of(NT) * kStaging + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
+  const int fixed = 1024 + 96 + 16 * NT + readers_of(NT) * kStaging + 4 * (3 * a.E + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1);
   constexpr int kSteps = steps_of(NT);
   a.w_stages = (kLimit - fixed - kSteps * kXStage) / kWStage;
   if (a.w_stages > 12) a.w_stages = 12;

@@ -568,6 +568,22 @@ def test_expert_layer(finalize):
         m.norm(normal(g, b + 5, H), None)
 
 
+def test_expert_layer_without_tokens_and_without_local_experts():
+    g = gen(11)
+    E, K, H, I = 8, 2, 256, 128
+    for finalize in (True, False):
+        m = layer(g, 6, E, K, H, I, finalize)
+        none, out = filled(BF, 0, H), filled(BF, 0, H)
+        m.norm(none, none.clone())
+        m.experts(torch.empty((0, K), dtype=I32, device="cuda"), torch.empty((0, K), device="cuda"), out)
+        assert (m._offsets == 0).all()
+        x, out = normal(g, 6, H), filled(BF, 6, H)
+        m.norm(x, None)
+        m.experts(torch.full((6, K), -1, dtype=I32, device="cuda"), torch.ones((6, K), device="cuda"), out)
+        assert (out == 0).all()
+    assert mt.moe_tail_take_device_error() == 0
+
+
 def test_expert_layer_in_a_graph_and_on_a_side_stream():
     g = gen(6)
     b, E, K, H, I = 24, 16, 4, 256, 128

@@ -150,7 +150,7 @@ def plan(rows, experts):
     """(weight stages, steps, halves of a step, accumulators) as the library launches a tile of so many rows."""
     halves, steps = (1, 5) if rows > 128 else (2, (512 - 2 * rows) // 64)
     readers = 2 if rows > 128 else 1
-    fixed = 1024 + 32 + 16 * rows + readers * 4096 + 4 * (3 * experts + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1)
+    fixed = 1024 + 96 + 16 * rows + readers * 4096 + 4 * (3 * experts + 1) + 8 * (2 * 12 + 3 * 15 + 2 * 2 + 1)
     stages = min(12, (227 * 1024 - fixed - steps * halves * rows * 128) // 16384)
     return stages - stages % (SETS * halves // 2), steps, halves, 1 if rows > 128 else 2
 
