@@ -127,25 +127,27 @@ def _stream(stream):
 
 def _cuda(*ts):
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
 def _dims(name: str, t, n: int) -> tuple:
     """The shape of t, which must have n dimensions."""
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 def _like(name: str, t, dtype, shape) -> None:
     """t must be dtype with exactly this shape: the C entry points receive only
     a pointer and take the layout from the sizes, so a tensor of another type
     or shape would be read (or written) as if it had this one."""
+    if t.dtype == dtype and t.shape == shape:
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _finalize_args(kind: str, src, permuted_idx, route_weights, gamma, out) -> tuple:
@@ -419,13 +421,14 @@ def moe_shared_expert(x, w_gate, w_up, w_down, out, workspace, *, accumulate=Tru
 def _eight_bits(q, scale, rows: int, width: int, group: int) -> int:
     """The type code of 8-bit rows q [rows, width] and their FP32 scales: [rows]
     (group 0) or [rows, ceil(width / 128)] (group 128)."""
-    if q.dtype not in Q_DTYPES:
+    kind = Q_DTYPES.get(q.dtype)
+    if kind is None:
         raise ValueError(f"q must be torch.int8 or torch.float8_e4m3fn, got {q.dtype}")
-    if group not in (0, QUANT_GROUP):
+    if group != 0 and group != QUANT_GROUP:
         raise ValueError(f"group must be 0 (one scale a row) or {QUANT_GROUP}, got {group}")
     _like("q", q, q.dtype, (rows, width))
     _like("scale", scale, torch.float32, (rows, -(-width // group)) if group else (rows,))
-    return Q_DTYPES[q.dtype]
+    return kind
 
 
 def moe_tail_norm_quant(x, residual, gamma, q, scale, *, residual_out=None, y=None, gain_center=1.0, eps=1e-6, group=0,
@@ -435,12 +438,15 @@ def moe_tail_norm_quant(x, residual, gamma, q, scale, *, residual_out=None, y=No
     group=128 [b, ceil(H / 128)]); x, residual BF16 [b, H] (residual may be
     None), gamma BF16 [H].  residual_out (BF16 [b, H], may be x or residual)
     receives bf16(h), y the normed row in BF16.  Returns (q, scale)."""
-    b, H = _dims("x", x, 2)
-    _like("x", x, torch.bfloat16, (b, H))
+    shape = b, H = _dims("x", x, 2)
+    _like("x", x, torch.bfloat16, shape)
     _like("gamma", gamma, torch.bfloat16, (H,))
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None:
-            _like(name, t, torch.bfloat16, (b, H))
+    if residual is not None:
+        _like("residual", residual, torch.bfloat16, shape)
+    if residual_out is not None:
+        _like("residual_out", residual_out, torch.bfloat16, shape)
+    if y is not None:
+        _like("y", y, torch.bfloat16, shape)
     kind = _eight_bits(q, scale, b, H, group)
     _cuda(x, residual, gamma, q, scale, residual_out, y)
     _check("moe_tail_norm_quant", lib().moe_tail_norm_quant(
