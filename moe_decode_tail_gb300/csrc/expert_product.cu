@@ -346,10 +346,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   // [my_begin, my_end) of them to this thread block; then come whole tiles, one in gridDim.x.
   const int64_t tiles = (int64_t)s_first[a.E] * m_tiles;
   // Dealing saves the idle part of a last wave, w_blocks * (1 - odd / grid) reduction blocks, and costs the FP32
-  // sums' way through memory: about one reduction block's time for 16 rows (16 rows, 2016 tiles: 206 -> 200 us; 256
-  // rows, about 3000 tiles: 735 us without it, 807 with it).
+  // sums' way through memory, measured as about ten blocks' time and one for 8 rows: 16 tiles of 32 blocks (2048 x
+  // 4096) took 15 us dealt out and 19 not with 8 rows, 20 and 25 with 100; 56 tiles of 28 blocks (7168 x 3584) 17.8 and
+  // 18.6 with 8 rows, 26 and 23 with 100; 64 tiles of 16 blocks were never better dealt out.
   const int odd = (int)(tiles % gridDim.x);
-  const int64_t dealt = (int64_t)a.w_blocks * (gridDim.x - odd) > (int64_t)(NT / 16) * gridDim.x ? odd : 0;
+  const int64_t dealt = (int64_t)a.w_blocks * (gridDim.x - odd) > (int64_t)(10 + NT / 8) * gridDim.x ? odd : 0;
   const int64_t total = dealt * a.w_blocks;
   const int64_t worth = (total + kLeastBlocks - 1) / kLeastBlocks;
   const int64_t grid = worth < gridDim.x ? worth : gridDim.x;  // thread blocks with dealt work
@@ -696,11 +697,12 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
 // ---- host ----------------------------------------------------------------------------
 
 // Rows of a tile: all of them where one expert has few, else twice an expert's average share, so that an uneven
-// batch still has one row tile for most experts.  (128 experts, 32 rows each on average: 200 us with tiles of 64,
-// 243 with tiles of 256; at 256 each, 500 us with 256.)
+// batch still has one row tile for most experts.  Tiles of 128 go further, up to twice as many rows: they have a
+// second accumulator and half the steps (128 experts of 2048 x 4096: 128 rows each on average 316 us, 349 with tiles of
+// 256; 32 rows each 200 us with 64, 243 with 256; 256 rows each 508 us with 256, 537 with 128).
 int rows_of_tile(int64_t R, int E) {
   const int64_t want = E == 1 ? R : 2 * ((R + E - 1) / E);
-  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 256 ? 128 : 256;
 }
 
 size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
