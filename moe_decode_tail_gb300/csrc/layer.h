@@ -82,7 +82,7 @@ struct DispatchArgs {
   int64_t num_rows;
   int b, K, row_bytes;
 };
-cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_dispatch_rows(const DispatchArgs& a, cudaStream_t stream);
 
 struct CombineArgs {
   const uint16_t* rows;   // BF16 [num_rows][H]
@@ -95,8 +95,8 @@ struct CombineArgs {
   uint16_t* d_rows;       // gradient: BF16 [num_rows][H]
   float* d_w;             // gradient: [b][K]
 };
-cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, int sms, cudaStream_t stream);
-cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, int sms, cudaStream_t stream);
+cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, cudaStream_t stream);
+cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, cudaStream_t stream);
 
 // ---- 8-bit product (expert_product.cu) -------------------------------------------
 

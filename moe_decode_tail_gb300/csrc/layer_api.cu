@@ -163,7 +163,7 @@ MOE_API int moe_tail_dispatch_rows(const void* x, const void* scale, const int32
   a.b = b;
   a.K = K;
   a.row_bytes = (int)row;
-  return finish(moetail::launch_dispatch_rows(a, device_sms(), static_cast<cudaStream_t>(stream)));
+  return finish(moetail::launch_dispatch_rows(a, static_cast<cudaStream_t>(stream)));
 }
 
 MOE_API int moe_tail_combine_rows(const void* rows, int64_t num_rows, const int32_t* permuted_idx,
@@ -190,7 +190,7 @@ MOE_API int moe_tail_combine_rows(const void* rows, int64_t num_rows, const int3
   const int wmode = !route_weights ? moetail::kWeightUnit
                     : weight_dtype == MOE_TAIL_W_BF16 ? moetail::kWeightBF16
                                                       : moetail::kWeightF32;
-  return finish(moetail::launch_combine_rows(a, wmode, device_sms(), static_cast<cudaStream_t>(stream)));
+  return finish(moetail::launch_combine_rows(a, wmode, static_cast<cudaStream_t>(stream)));
 }
 
 MOE_API int moe_tail_combine_grad(const void* d_out, const void* rows, int64_t num_rows, const int32_t* permuted_idx,
@@ -219,7 +219,7 @@ MOE_API int moe_tail_combine_grad(const void* d_out, const void* rows, int64_t n
   a.d_rows = static_cast<uint16_t*>(d_rows);
   a.d_w = static_cast<float*>(d_weights);
   const int wmode = weight_dtype == MOE_TAIL_W_BF16 ? moetail::kWeightBF16 : moetail::kWeightF32;
-  return finish(moetail::launch_combine_grad(a, wmode, device_sms(), static_cast<cudaStream_t>(stream)));
+  return finish(moetail::launch_combine_grad(a, wmode, static_cast<cudaStream_t>(stream)));
 }
 
 // ============================================================================ 8-bit product

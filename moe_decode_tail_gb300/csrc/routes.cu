@@ -346,7 +346,7 @@ cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t stream) {
   }
 }
 
-cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_dispatch_rows(const DispatchArgs& a, cudaStream_t stream) {
   const bool wide = a.row_bytes % 16 == 0;
   const int nv = a.row_bytes / (wide ? 16 : 8);
   const dim3 grid(a.b, (nv + 255) / 256);
@@ -354,7 +354,7 @@ cudaError_t launch_dispatch_rows(const DispatchArgs& a, int sms, cudaStream_t st
   return launch_pdl(dispatch_rows_kernel<uint2>, grid, dim3(256), 0, stream, a);
 }
 
-cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
+cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, cudaStream_t stream) {
   const int nv = a.H >> 3;
   // Small blocks: 64 threads took 83 us where 256 took 86 (8191 tokens, 16 routes, 3584 columns), and at 64 tokens
   // they spread a row over more SMs.
@@ -365,7 +365,7 @@ cudaError_t launch_combine_rows(const CombineArgs& a, int wmode, int sms, cudaSt
   return launch_pdl(combine_rows_kernel<kWeightF32>, grid, dim3(threads), 0, stream, a);
 }
 
-cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, int sms, cudaStream_t stream) {
+cudaError_t launch_combine_grad(const CombineArgs& a, int wmode, cudaStream_t stream) {
   const int nv = a.H >> 3;
   // Two vectors a thread: 96 us for 4096 tokens, 8 routes, 4096 columns; one or four: 103 and 104.  More only where
   // a block of 1024 threads needs them.

@@ -247,8 +247,9 @@ int threads_for(int nv, int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32;
 // Vectors a thread: one where the rows are fewer than the SMs can take at once (a row's latency counts), else `many`,
 // more where the row does not fit a block otherwise.
 int vectors_for(int nv, int64_t rows, int sms, int many) {
-  int vpt = rows <= 2 * sms ? 1 : many;
-  while (threads_for(nv, vpt) > (vpt == 1 ? 1024 : 512)) vpt *= 2;
+  if (rows <= 2 * sms && nv <= 1024) return 1;
+  int vpt = many;
+  while (threads_for(nv, vpt) > 512) vpt *= 2;
   return vpt;
 }
 
@@ -266,7 +267,7 @@ cudaError_t launch_norm_quant(const NormQuantArgs& a, int kind, bool grouped, in
                                  : launch(norm_quant_kernel<kQuantE4M3, false, VPT>, VPT)))
   // 16384 rows of 4096: 81 us with four vectors a thread, 91 with two, 100 with one.
   const int vpt = vectors_for(nv, a.b, sms, 4);
-  return vpt == 1 ? MOE_PICK(1) : vpt == 2 ? MOE_PICK(2) : vpt == 4 ? MOE_PICK(4) : MOE_PICK(8);
+  return vpt == 1 ? MOE_PICK(1) : vpt == 4 ? MOE_PICK(4) : MOE_PICK(8);
 #undef MOE_PICK
 }
 

@@ -645,3 +645,56 @@ def test_large_offsets():
     assert not d_rows[1:R - 3].any()
     mt.moe_tail_dispatch_rows(out, idx, rows)
     assert torch.equal(rows[R - 1], out[0]) and torch.equal(rows[R - 2], out[1]) and torch.equal(rows[0], out[0])
+
+
+class Guarded:
+    """Output tensors inside larger buffers, whose other bytes must stay as they are."""
+
+    def __init__(self):
+        self.buffers = []
+
+    def __call__(self, dtype, *shape, align=256):
+        n = int(torch.tensor([], dtype=dtype).element_size() * torch.Size(shape).numel())
+        pad = 1 << 16
+        whole = torch.full((pad + n + pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        start = pad + (-(whole.data_ptr() + pad)) % align
+        self.buffers.append((whole, start, n))
+        return whole[start:start + n].view(dtype).view(shape)
+
+    def intact(self):
+        return all((w[:s] == 0xA5).all() and (w[s + n:] == 0xA5).all() for w, s, n in self.buffers)
+
+
+@pytest.mark.parametrize("b,K,E,H,N", [(1, 1, 1, 16, 8), (3, 2, 5, 48, 24), (37, 3, 9, 272, 136), (130, 4, 16, 1040, 392),
+                                       (513, 6, 60, 528, 200), (700, 2, 3, 4112, 1032)])
+def test_nothing_outside_the_outputs_is_written(b, K, E, H, N):
+    g, new = gen(b + H), Guarded()
+    R = b * K
+    x, res, gamma = normal(g, b, H), normal(g, b, H), normal(g, H)
+    for dtype, group in ((I8, 0), (E4, 128)):
+        scale = [b] if not group else [b, -(-H // 128)]
+        mt.moe_tail_norm_quant(x, res, gamma, new(dtype, b, H), new(F32, *scale), residual_out=new(BF, b, H),
+                               y=new(BF, b, H), group=group)
+        mt.moe_tail_silu_quant(normal(g, b, 2 * H), new(dtype, b, H), new(F32, *scale), group=group)
+    ids, _ = routes(g, b, K, E, local=0.8)
+    offsets, idx, source = new(I32, E + 1), new(I32, b, K), new(I32, R)
+    mt.moe_tail_sort_routes(ids, offsets, idx, source, new(torch.uint8, mt.moe_tail_sort_workspace_bytes(b, K, E)))
+    for got, want in zip((offsets, idx, source), plain_sort(ids, E)):
+        assert torch.equal(got, want)
+    x8, xs = int8(g, b, H), scales(g, b)
+    rows8, row_scale = new(I8, R, H), new(F32, R)
+    mt.moe_tail_dispatch_rows(x8, idx, rows8, scale=xs, row_scale=row_scale)
+    mt.moe_tail_dispatch_rows(x, idx, new(BF, R, H))
+    w = torch.softmax(normal(g, b, K, dtype=F32), 1)
+    rows = normal(g, R, H)
+    mt.moe_tail_combine_rows(rows, idx, w, new(BF, b, H))
+    mt.moe_tail_combine_grad(x, rows, idx, w, new(BF, R, H), new(F32, b, K))
+    wide, ws = int8(g, E, N, H), scales(g, E, N)
+    mt.moe_tail_expert_product(rows8, row_scale, wide, ws, new(BF, R, N),
+                               new(torch.uint8, mt.moe_tail_expert_product_workspace_bytes(R, E, N, H)),
+                               expert_offsets=offsets)
+    mt.moe_tail_expert_product(x8, xs, wide[:1], ws[:1], new(BF, b, N),
+                               new(torch.uint8, mt.moe_tail_expert_product_workspace_bytes(b, 1, N, H)))
+    torch.cuda.synchronize()
+    assert new.intact()
+    assert mt.moe_tail_take_device_error() == 0
