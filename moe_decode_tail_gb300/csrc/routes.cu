@@ -168,20 +168,19 @@ template <typename V>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(const DispatchArgs a) {
   grid_dependency_wait();
   launch_dependents();
-  const int t = blockIdx.x;
-  const int nv = a.row_bytes / (int)sizeof(V);
-  const V* src = reinterpret_cast<const V*>(a.x) + (int64_t)t * nv;
-  for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
-    const V d = src[v];
-    for (int k = 0; k < a.K; ++k) {
-      const int64_t j = a.idx[(int64_t)t * a.K + k];
-      if (j >= 0 && j < a.num_rows) reinterpret_cast<V*>(a.rows)[j * nv + v] = d;
-    }
+  const int64_t t = blockIdx.x;
+  const int nv = a.row_bytes / (int)sizeof(V), lane = threadIdx.x & 31;
+  const int v = blockIdx.y * blockDim.x + threadIdx.x;
+  // lane k keeps route k's row, -1 without one
+  int mine = lane < a.K ? a.idx[t * a.K + lane] : -1;
+  if (mine >= a.num_rows) mine = -1;
+  V d = {};
+  if (v < nv) d = static_cast<const V*>(a.x)[t * nv + v];
+  for (int k = 0; k < a.K; ++k) {
+    const int64_t j = __shfl_sync(0xffffffffu, mine, k);
+    if (j >= 0 && v < nv) static_cast<V*>(a.rows)[j * nv + v] = d;
   }
-  if (a.scale && blockIdx.y == 0 && threadIdx.x < a.K) {
-    const int64_t j = a.idx[(int64_t)t * a.K + threadIdx.x];
-    if (j >= 0 && j < a.num_rows) a.row_scale[j] = a.scale[t];
-  }
+  if (a.scale && v < 32 && mine >= 0) a.row_scale[mine] = a.scale[t];
 }
 
 template <int WMODE>
