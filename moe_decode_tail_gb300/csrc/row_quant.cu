@@ -11,7 +11,7 @@
 // the rounding, so every input is read once.  The norm is bound by memory, 4 + 2 + 1 bytes a column: 16384 rows of
 // 4096 in 74 us, 6.3 TB/s (0.93 of the measured copy rate).  silu reads and writes 4 + 1 bytes a column and is
 // bound by its exponential, reciprocal and conversions nearly as much: 28672 rows of 2048 in e4m3 with a scale for
-// every 128 columns in 54 us, 5.4 TB/s (0.80), three quarters of the issue slots taken.  One token of 7168 columns
+// every 128 columns in 59 us, 5.0 TB/s (0.74).  One token of 7168 columns
 // takes 4.5 us, a launch and two trips to memory.
 #include <cuda_fp8.h>
 
@@ -204,9 +204,33 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
   store_rows<KIND, GROUPED, VPT>(h, largest, row, nv, a.q, a.scale, a.groups);
 }
 
-// silu by the fast exponential and division: both are within a few units in the last place, far below a step of
-// 8 bits, and exact ones cost more time than the row's memory traffic.
-__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(d);
+}
+
+// silu(g) * up = g * up / (1 + exp(-g)) for two columns, within 10 units in the last place.  With e = exp(-|g| / 2): for
+// g >= 0 the divisor is 1 + e^2; for g < 0 the fraction is multiplied by e^2 above and below, one e with each factor, so
+// that nothing leaves FP32's range before the result does.
+// The exponential: a BF16 |g| times the upper 16 bits of log2(e) / 2 is exact (t), and what that leaves of the exponent,
+// at most 175 * 3.6e-6, multiplies the power of two by 1 + (rest) ln 2; zero from |g| = 175 on.  One exponent rounded to
+// FP32 would be off by up to |g| units.
+__device__ __forceinline__ float2 silu_times(float2 g, float2 up) {
+  constexpr double kHalfLog2e = 0.72134752044448170368, kLn2 = 0.69314718055994530942;
+  constexpr float kUpper = 47274.0f / 65536.0f;
+  constexpr float kRest = (float)((kHalfLog2e / kUpper - 1.0) * kLn2);  // of t
+  const float2 t = make_float2(-kUpper * fabsf(g.x), -kUpper * fabsf(g.y));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = fma2(e, mul2(t, splat2(kRest)), e);
+  const float2 divisor = fma2(e, e, splat2(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(divisor.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(divisor.y));
+  const float2 p = make_float2(g.x < 0.0f ? e.x : 1.0f, g.y < 0.0f ? e.y : 1.0f);
+  return mul2(mul2(mul2(g, p), mul2(up, p)), r);
+}
 
 template <int KIND, bool GROUPED, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) silu_quant_kernel(const SiluQuantArgs a) {
@@ -230,11 +254,15 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) silu_quant_kernel(const
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    float u[8];
-    unpack8(gate[i], y[i]);
-    unpack8(up[i], u);
+    float2 g[4], u[4];
+    unpack8p(gate[i], g);
+    unpack8p(up[i], u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[i][e] = silu_fast(y[i][e]) * u[e];
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = silu_times(g[e], u[e]);
+      y[i][2 * e] = v.x;
+      y[i][2 * e + 1] = v.y;
+    }
     if (!GROUPED) top = max(top, max8(y[i]));
   }
   if (!GROUPED) top = block_reduce(0.0f, top).top;
