@@ -14,6 +14,7 @@
 // every 128 columns in 59 us, 5.0 TB/s (0.74).  One token of 7168 columns
 // takes 4.5 us, a launch and two trips to memory.
 #include <cuda_fp8.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "layer.h"
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint32_t max_of_group(uint32_t m) {
   return m;
 }
 
-// Sum and maximum over the thread block, in a fixed order, known to every thread; called once in a kernel.
+// Sum and maximum over the thread block, in a fixed order, known to every thread; a barrier between two calls.
 struct RowSums {
   float sum;
   uint32_t top;
@@ -190,7 +191,34 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
     if (v < nv && a.residual_out) st_v4(a.residual_out + row * a.H + 8 * v, pack8_pz(h[i]));
   }
   const RowSums sums = block_reduce(sum, magnitude(top));
-  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(sums.sum * a.rcpH + a.eps));
+  float mean = sums.sum * a.rcpH + a.eps;
+  bool by_values = false;  // the row's maximum is to be taken of the values themselves
+  // Squares or their sum beyond FP32, or so small that they lost bits (a row near 1e19 or 1e-19): once more with the row
+  // brought near one by a power of two, which changes no bit and cancels in h * inv.
+  if (!(mean >= 0x1p-100f && mean <= FLT_MAX)) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) most = larger(most, __uint_as_float(max8(h[i])));
+    __syncthreads();
+    most = __uint_as_float(block_reduce(0.0f, magnitude(most)).top);
+    const float size = fmaxf(most, __fsqrt_rn(a.eps));
+    if (most <= FLT_MAX && size > 0.0f) {  // else the row has no finite norm
+      const int exponent = min(max((int)(magnitude(size) >> 23), 1), 253);
+      const float unit = __uint_as_float((uint32_t)(254 - exponent) << 23);  // size * unit is in [1, 4), or below one
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[i][e] *= unit;
+          sum += h[i][e] * h[i][e];
+        }
+      __syncthreads();
+      mean = block_reduce(sum, 0u).sum * a.rcpH + a.eps * unit * unit;
+      by_values = true;
+    }
+  }
+  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(mean));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
@@ -200,7 +228,14 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
     for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * inv) * (g[e] + a.gain_center);
     if (v < nv && a.y) st_v4(a.y + row * a.H + 8 * v, pack8_pz(h[i]));
   }
-  const uint32_t largest = magnitude(__uint_as_float(sums.top) * inv);
+  uint32_t largest = magnitude(__uint_as_float(sums.top) * inv);
+  if (!GROUPED && by_values) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) most = max(most, max8(h[i]));
+    __syncthreads();
+    largest = block_reduce(0.0f, most).top;
+  }
   store_rows<KIND, GROUPED, VPT>(h, largest, row, nv, a.q, a.scale, a.groups);
 }
 
