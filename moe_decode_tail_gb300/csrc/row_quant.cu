@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
       if (a.residual) res[i] = ld_rows(a.residual + row * a.H + 8 * v);
     }
   }
-  float h[VPT][8], sum = 0.0f, top = 0.0f;
+  float h[VPT][8], sum = 0.0f, top = 0.0f, most_gain = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
@@ -186,10 +186,14 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
     for (int e = 0; e < 8; ++e) {
       if (a.residual) h[i][e] += r[e];
       sum += h[i][e] * h[i][e];
-      if (!GROUPED) top = larger(top, h[i][e] * (g[e] + a.gain_center));
+      if (!GROUPED) {
+        top = larger(top, h[i][e] * (g[e] + a.gain_center));
+        most_gain = fmaxf(most_gain, fabsf(g[e] + a.gain_center));
+      }
     }
     if (v < nv && a.residual_out) st_v4(a.residual_out + row * a.H + 8 * v, pack8_pz(h[i]));
   }
+  if (most_gain >= 0x1p64f) top = __uint_as_float(0x7fffffffu);  // a NaN: see below
   const RowSums sums = block_reduce(sum, magnitude(top));
   float mean = sums.sum * a.rcpH + a.eps;
   bool by_values = false;  // the row's maximum is to be taken of the values themselves
@@ -228,8 +232,11 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
     for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * inv) * (g[e] + a.gain_center);
     if (v < nv && a.y) st_v4(a.y + row * a.H + 8 * v, pack8_pz(h[i]));
   }
-  uint32_t largest = magnitude(__uint_as_float(sums.top) * inv);
-  if (!GROUPED && by_values) {
+  // max|h * gain| * inv is max|(h * inv) * gain| but for a few units in the last place, as long as neither product leaves
+  // FP32's range nor loses bits below it: with inv in [2^-64, 2^50] and gains below 2^64 for results in these bounds.
+  const float estimate = __uint_as_float(sums.top) * inv;
+  uint32_t largest = magnitude(estimate);
+  if (!GROUPED && (by_values || !(estimate >= 0x1p-60f && estimate <= 0x1p126f))) {
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) most = max(most, max8(h[i]));

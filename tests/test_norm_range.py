@@ -107,3 +107,33 @@ def test_rows_without_a_norm():
         assert s[:3, 0].isnan().all() and s[3].isfinite().all()
     _, scale, _, _ = quantised(torch.zeros_like(x), None, gamma, I8, 0, eps=0.0)
     assert scale.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [I8, E4])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("H", SIZES)
+@pytest.mark.parametrize("size,gain,eps", [(1e18, 1e25, 1e-6), (1e3, 1e36, 1e-6), (1e30, 1e20, 1e-6), (1e-14, 1e-28, 1e-38),
+                                           (1e-3, 1e-34, 1e-9), (1.0, 1e-34, 1e-6), (1e-14, 1e30, 1e-38)])
+def test_products_with_gains_that_leave_the_range(size, gain, eps, H, group, dtype):
+    g = gen(H + 2)
+    x = (normal(g, 5, H) * size).to(BF)
+    x[2] = normal(g, H).to(BF)
+    gamma = (normal(g, H) * gain).to(BF)
+    check(quantised(x, None, gamma, dtype, group, gain_center=0.0, eps=eps), x, None, gamma, group, 0.0,
+          float(torch.tensor(eps, dtype=F32)))
+
+
+@pytest.mark.parametrize("dtype", [I8, E4])
+def test_a_row_and_its_only_group_agree(dtype):
+    # up to 128 columns a group is the row: whatever rounds on the way, both forms round the same values
+    g = gen(3)
+    H = 128
+    x, gamma = torch.full((3, H), 2.0 ** -87, device="cuda"), torch.full((H,), 2.0 ** 120, device="cuda")
+    x *= 1 + torch.rand((3, H), generator=g, device="cuda")
+    x[:, 0], gamma[0] = 2.0 ** 60, 0.0
+    x[1] *= 2.0 ** -40
+    x[2] *= 2.0 ** 40
+    x, gamma = x.to(BF), gamma.to(BF)
+    a = quantised(x, None, gamma, dtype, 0, gain_center=0.0, eps=1e-6)
+    b = quantised(x, None, gamma, dtype, 128, gain_center=0.0, eps=1e-6)
+    assert torch.equal(a[0].view(I8), b[0].view(I8)) and torch.equal(a[1], b[1][:, 0]) and torch.equal(a[3], b[3])
