@@ -463,7 +463,8 @@ int moe_tail_silu_quant(const void* gate_up, const int32_t* used_rows, int rows,
  *                       expert are in route order.
  *   source[row]         int32 [b * K]: the row's route, -1 past the last row
  *   workspace           >= moe_tail_sort_workspace_bytes(b, K, num_experts)
- *                       bytes, 16-byte aligned
+ *                       bytes, 16-byte aligned; a workspace for b tokens
+ *                       serves every smaller batch
  * b = 0 writes expert_offsets (zeros) and nothing else.
  * Limits: 1 <= K <= 32, b * K <= 2^21, num_experts <= 1024.
  */

@@ -62,6 +62,8 @@ cudaError_t launch_silu_quant(const SiluQuantArgs& a, int kind, bool grouped, in
 // ---- routes (routes.cu) ----------------------------------------------------------
 
 int sort_blocks(int routes);  // thread blocks of a sort, each with a row of counts in the workspace
+// The most of any sort of so many routes or fewer: sort_blocks falls from 128 to 33 where a lane takes four times as many.
+int sort_blocks_up_to(int routes);
 
 struct SortArgs {
   const int32_t* ids;     // [routes]

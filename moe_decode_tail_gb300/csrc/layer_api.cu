@@ -117,7 +117,7 @@ MOE_API int moe_tail_silu_quant(const void* gate_up, const int32_t* used_rows, i
 
 MOE_API size_t moe_tail_sort_workspace_bytes(int b, int K, int num_experts) {
   if (!routes_ok(b, K) || (int64_t)b * K > kMaxRoutes || num_experts < 1 || num_experts > kMaxExperts) return 0;
-  return round256((size_t)4 * moetail::sort_blocks(b * K) * num_experts);
+  return round256((size_t)4 * moetail::sort_blocks_up_to(b * K) * num_experts);
 }
 
 MOE_API int moe_tail_sort_routes(const int32_t* expert_ids, int b, int K, int num_experts, int32_t* expert_offsets,

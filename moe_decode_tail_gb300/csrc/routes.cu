@@ -327,14 +327,23 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
                     a);
 }
 
-// Routes of a lane: few, until there would be more than 128 chunks (each thread block adds up the counts of all).
-int routes_of_lane(int routes) { return routes <= 128 * 1024 ? 1 : routes <= 4 * 128 * 1024 ? 4 : 16; }
+constexpr int kMostBlocks = 128;  // each thread block adds up the counts of all
+
+// Routes of a lane: few, until there would be more blocks.
+int routes_of_lane(int routes) {
+  return routes <= kMostBlocks * kSortThreads ? 1 : routes <= 4 * kMostBlocks * kSortThreads ? 4 : 16;
+}
 
 }  // namespace
 
 int sort_blocks(int routes) {
   const int chunk = kSortThreads * routes_of_lane(routes);
   return routes > chunk ? (routes + chunk - 1) / chunk : 1;
+}
+
+int sort_blocks_up_to(int routes) {
+  const int64_t of_one = ((int64_t)routes + kSortThreads - 1) / kSortThreads;  // chunks of one route a lane
+  return of_one < 1 ? 1 : of_one < kMostBlocks ? (int)of_one : kMostBlocks;
 }
 
 cudaError_t launch_sort_routes(const SortArgs& a, cudaStream_t stream) {
