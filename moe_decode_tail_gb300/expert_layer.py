@@ -35,7 +35,10 @@ def quantise_channels(w):
 class ExpertLayerI8:
     """gamma BF16 [H]; w_gate_up int8 [E, 2 I, H] (the I gate channels before the up channels) with scales FP32
     [E, 2 I]; w_down int8 [E, H, I] with scales FP32 [E, H].  finalize_gamma (BF16 [H]): the route rows are normalised
-    with it before they are weighted and summed (moe_tail_ep_finalize); None: they are not (moe_tail_combine_rows)."""
+    with it before they are weighted and summed (moe_tail_ep_finalize); None: they are not (moe_tail_combine_rows).
+
+    A layer keeps the rows of a norm() for its experts() in buffers of its own, so one layer serves one stream and one
+    thread at a time."""
 
     def __init__(self, gamma, w_gate_up, s_gate_up, w_down, s_down, *, max_tokens, top_k, finalize_gamma=None,
                  gain_center=1.0, eps=1e-6):
@@ -45,6 +48,7 @@ class ExpertLayerI8:
         self.gamma, self.finalize_gamma = gamma, finalize_gamma
         self.w_gate_up, self.s_gate_up, self.w_down, self.s_down = w_gate_up, s_gate_up, w_down, s_down
         self.max_tokens, self.K, self.gain_center, self.eps = max_tokens, top_k, gain_center, eps
+        self._normed = None  # tokens of the last norm()
         dev, rows, I = gamma.device, max_tokens * top_k, self.I2 // 2
 
         def new(dtype, *shape):
@@ -68,14 +72,19 @@ class ExpertLayerI8:
         b = self._tokens(x)
         if residual_out is None:
             residual_out = residual
+        self._normed = None
         moe_tail_norm_quant(x, residual, self.gamma, self._q[:b], self._scale[:b], residual_out=residual_out, y=y,
                             gain_center=self.gain_center, eps=self.eps)
+        self._normed = b
         return residual_out
 
     def experts(self, expert_ids, route_weights, out) -> torch.Tensor:
-        """The experts' contribution for the rows of the last norm() into out (BF16 [b, H]); expert_ids int32 [b, K]
-        (an id outside [0, E): not one of this layer's experts), route_weights [b, K]."""
+        """The experts' contribution for the rows of the last norm() into out (BF16 [b, H]); expert_ids int32 [b, K] for
+        that norm's b tokens (an id outside [0, E): not one of this layer's experts), route_weights [b, K]."""
         b, R = self._tokens(expert_ids), expert_ids.shape[0] * self.K
+        if b != self._normed:
+            raise ValueError(f"routes of {b} tokens, and the rows are those of "
+                             + ("no norm()" if self._normed is None else f"a norm() of {self._normed}"))
         idx, used = self._idx[:b], self._offsets[self.E:]
         x, h, rows = (t[:R] for t in (self._x, self._h, self._rows))
         moe_tail_sort_routes(expert_ids, self._offsets, idx, self._source[:R], self._workspace)
