@@ -19,11 +19,15 @@ from __future__ import annotations
 
 import torch
 
-from . import (moe_tail_combine_rows, moe_tail_dispatch_rows, moe_tail_ep_finalize, moe_tail_expert_product,
+from . import (_like, moe_tail_combine_rows, moe_tail_dispatch_rows, moe_tail_ep_finalize, moe_tail_expert_product,
                moe_tail_expert_product_workspace_bytes, moe_tail_norm_quant, moe_tail_silu_quant, moe_tail_sort_routes,
                moe_tail_sort_workspace_bytes)
 
 __all__ = ["ExpertLayerI8", "quantise_channels"]
+
+MAX_WIDTH = 32768            # columns of a row in 8 bits
+MAX_ROUTES = 1 << 21         # of one sort
+MAX_FINALIZE_TOKENS = 65535
 
 
 def quantise_channels(w):
@@ -43,8 +47,16 @@ class ExpertLayerI8:
     def __init__(self, gamma, w_gate_up, s_gate_up, w_down, s_down, *, max_tokens, top_k, finalize_gamma=None,
                  gain_center=1.0, eps=1e-6):
         self.E, self.I2, self.H = w_gate_up.shape
-        if self.I2 % 16 or tuple(w_down.shape) != (self.E, self.H, self.I2 // 2):
+        if self.I2 % 2 or tuple(w_down.shape) != (self.E, self.H, self.I2 // 2):
             raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not belong together")
+        workspace = self._workspace_bytes(max_tokens, top_k, finalize_gamma is not None)
+        for name, t, dtype, shape in (
+                ("gamma", gamma, torch.bfloat16, (self.H,)), ("w_gate_up", w_gate_up, torch.int8, w_gate_up.shape),
+                ("s_gate_up", s_gate_up, torch.float32, (self.E, self.I2)), ("w_down", w_down, torch.int8, w_down.shape),
+                ("s_down", s_down, torch.float32, (self.E, self.H)),
+                ("finalize_gamma", finalize_gamma, torch.bfloat16, (self.H,))):
+            if t is not None:
+                _like(name, t, dtype, shape)
         self.gamma, self.finalize_gamma = gamma, finalize_gamma
         self.w_gate_up, self.s_gate_up, self.w_down, self.s_down = w_gate_up, s_gate_up, w_down, s_down
         self.max_tokens, self.K, self.gain_center, self.eps = max_tokens, top_k, gain_center, eps
@@ -61,10 +73,21 @@ class ExpertLayerI8:
         self._gate_up = new(torch.bfloat16, rows, self.I2)
         self._h, self._h_scale = new(torch.int8, rows, I), new(torch.float32, rows)
         self._rows = new(torch.bfloat16, rows, self.H)
-        self._workspace = new(torch.uint8, max(
-            moe_tail_sort_workspace_bytes(max_tokens, top_k, self.E),
-            moe_tail_expert_product_workspace_bytes(rows, self.E, self.I2, self.H),
-            moe_tail_expert_product_workspace_bytes(rows, self.E, self.H, I)))
+        self._workspace = new(torch.uint8, workspace)
+
+    def _workspace_bytes(self, tokens, K, finalize) -> int:
+        """What the calls need of workspace for so many tokens; ValueError for sizes that one of them does not take."""
+        H, I, rows = self.H, self.I2 // 2, tokens * K
+        sort = moe_tail_sort_workspace_bytes(tokens, K, self.E) if 0 <= rows <= MAX_ROUTES else 0
+        if sort == 0:
+            raise ValueError(f"{tokens} tokens of {K} routes each over {self.E} experts: 1 to 32 routes a token, {MAX_ROUTES} "
+                             "in all and 1 to 1024 experts")
+        products = [moe_tail_expert_product_workspace_bytes(rows, self.E, N, D) for N, D in ((self.I2, H), (H, I))]
+        if max(H, I) > MAX_WIDTH or 0 in products:
+            raise ValueError(f"H = {H} and I = {I} must be multiples of 16 up to {MAX_WIDTH}")
+        if finalize and tokens > MAX_FINALIZE_TOKENS:
+            raise ValueError(f"{tokens} tokens: moe_tail_ep_finalize takes at most {MAX_FINALIZE_TOKENS}")
+        return max(sort, *products)
 
     def norm(self, x, residual, *, y=None, residual_out=None):
         """x + residual normalised into the layer's int8 rows; residual_out (by default in place, where there is a

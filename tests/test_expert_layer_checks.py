@@ -55,3 +55,47 @@ def test_a_refused_norm_leaves_no_rows_to_use():
     for b in (3, 5):
         with pytest.raises(ValueError, match="norm"):
             m.experts(*routes(b, device="cuda"))
+
+
+# ---- sizes ---------------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("sizes", [dict(I=24), dict(I=8), dict(H=72), dict(H=520), dict(H=8), dict(K=0), dict(K=33),
+                                   dict(tokens=-1), dict(E=1025, H=16, I=16), dict(H=32784, I=16, E=1), dict(I=32784, H=16, E=1),
+                                   dict(tokens=(1 << 20) + 1)])
+def test_sizes_that_a_call_would_refuse(sizes):
+    with pytest.raises(ValueError):
+        layer(**sizes)
+
+
+def test_tokens_beyond_the_finalize_call():
+    gamma = torch.zeros(16, dtype=BF)
+    sizes = dict(E=1, H=16, I=16, K=1)
+    assert layer(tokens=65535, finalize_gamma=gamma, **sizes).max_tokens == 65535
+    assert layer(tokens=65536, **sizes).max_tokens == 65536  # the plain weighted sum takes them
+    with pytest.raises(ValueError, match="65535"):
+        layer(tokens=65536, finalize_gamma=gamma, **sizes)
+
+
+def test_operands_of_another_type_or_shape():
+    E, H, I = 4, 64, 32
+    good = dict(gamma=torch.zeros(H, dtype=BF), w_gate_up=torch.ones((E, 2 * I, H), dtype=I8), s_gate_up=torch.ones((E, 2 * I)),
+                w_down=torch.ones((E, H, I), dtype=I8), s_down=torch.ones((E, H)), finalize_gamma=torch.zeros(H, dtype=BF))
+    ExpertLayerI8(**good, max_tokens=2, top_k=2)
+    for name, old in good.items():
+        for new in (old.to(torch.float64), torch.zeros([s + 16 for s in old.shape], dtype=old.dtype)):
+            with pytest.raises(ValueError):
+                ExpertLayerI8(**{**good, name: new}, max_tokens=2, top_k=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,H,I,K", [(1, 16, 16, 1), (1024, 32, 16, 2), (2, 32768, 16, 1), (2, 16, 32768, 2), (3, 48, 80, 32)])
+def test_sizes_at_the_limits_run(E, H, I, K):
+    for finalize in (None, torch.zeros(H, dtype=BF, device="cuda")):
+        m = layer(E=E, H=H, I=I, tokens=3, K=K, device="cuda", finalize_gamma=finalize)
+        x, out = torch.ones((3, H), dtype=BF, device="cuda"), torch.empty((3, H), dtype=BF, device="cuda")
+        m.norm(x, None)
+        ids = (torch.arange(3 * K, device="cuda") % E).to(I32).view(3, K)
+        m.experts(ids, torch.full((3, K), 1.0 / K, device="cuda"), out)
+        torch.cuda.synchronize()
+        assert out.isfinite().all()
