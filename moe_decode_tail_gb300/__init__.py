@@ -120,8 +120,11 @@ def _p(t):
 
 
 def _stream(stream):
-    if stream is None:  # the current stream's handle, without making a Stream object for it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        try:  # the current stream's handle, without making a Stream object for it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:  # a torch without these functions, which are not public
+            stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
