@@ -419,7 +419,8 @@ int moe_tail_set_stage_wait_limit(unsigned long long limit_ns);
  * with FP32 scales per group: the whole row (group = 0, scale [rows]) or 128
  * columns (group = 128, scale [rows][ceil(width / 128)], the last group
  * shorter).  A value is q * scale.  With M = 127 (int8) or 448 (e4m3):
- *   scale = max|y| / M,  q = round(y / scale), to nearest even, |q| <= M
+ *   scale = max|y| / M,  q = round(y * (M / max|y|)), to nearest even, |q| <= M
+ * (FP32; y / scale may fall on the other side of a rounding).
  * A group of zeros has scale 0 and q = 0; a group with a NaN or an infinity
  * has scale NaN and q = 0, so that what is computed from it is NaN.
  */
@@ -515,7 +516,10 @@ int moe_tail_combine_grad(const void* d_out, const void* rows, int64_t num_rows,
  * 8-bit integer product with a scale for each row and each channel, by expert:
  *   out[r][n] = bf16( (sum over k of x[r][k] * w[e][n][k]) * w_scale[e][n] * x_scale[r] )
  * for the rows r of [expert_offsets[e], expert_offsets[e + 1]).  Rows of no
- * expert are not written.
+ * expert are not written.  The products of int8 are added in FP32, not in whole
+ * numbers: the sum is exact while the magnitudes of its terms add up to at most
+ * 2^24 (always up to D = 1024), and beyond that rounded as it grows, by at most
+ * D * 2^-24 of those magnitudes in all.
  *   x         int8 [rows][D]          x_scale  FP32 [rows]
  *   w         int8 [num_experts][N][D]  w_scale  FP32 [num_experts][N]
  *   expert_offsets  device int32 [num_experts + 1], ascending within [0, rows]

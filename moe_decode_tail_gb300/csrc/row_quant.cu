@@ -9,10 +9,10 @@
 //
 // A thread block per row, 16-byte loads of 8 columns; the values stay in registers between the reduction and
 // the rounding, so every input is read once.  The norm is bound by memory, 4 + 2 + 1 bytes a column: 16384 rows of
-// 4096 in 74 us, 6.3 TB/s (0.93 of the measured copy rate).  silu reads and writes 4 + 1 bytes a column and is
-// bound by its exponential, reciprocal and conversions nearly as much: 28672 rows of 2048 in e4m3 with a scale for
-// every 128 columns in 59 us, 5.0 TB/s (0.74).  One token of 7168 columns
-// takes 4.5 us, a launch and two trips to memory.
+// 4096 in 75.5 us, 6.2 TB/s (0.92 of the measured copy rate).  silu reads and writes 4 + 1 bytes a column and is
+// bound by its exponential, reciprocal and conversions as much: 28672 rows of 2048 in 55 us in int8 with a scale a
+// row, 59 us, 5.0 TB/s (0.73), in e4m3 with a scale for every 128 columns.  One token of 7168 columns takes 4.5 us, a
+// launch and two trips to memory.
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -335,7 +335,7 @@ cudaError_t launch_norm_quant(const NormQuantArgs& a, int kind, bool grouped, in
                                  : launch(norm_quant_kernel<kQuantInt8, false, VPT>, VPT))                   \
                       : (grouped ? launch(norm_quant_kernel<kQuantE4M3, true, VPT>, VPT)                     \
                                  : launch(norm_quant_kernel<kQuantE4M3, false, VPT>, VPT)))
-  // 16384 rows of 4096: 81 us with four vectors a thread, 91 with two, 100 with one.
+  // 16384 rows of 4096: 75.5 us with four vectors a thread, 81 with two, 88 with one.
   const int vpt = vectors_for(nv, a.b, sms, 4);
   return vpt == 1 ? MOE_PICK(1) : vpt == 4 ? MOE_PICK(4) : MOE_PICK(8);
 #undef MOE_PICK
@@ -351,7 +351,7 @@ cudaError_t launch_silu_quant(const SiluQuantArgs& a, int kind, bool grouped, in
                                  : launch(silu_quant_kernel<kQuantInt8, false, VPT>, VPT))                   \
                       : (grouped ? launch(silu_quant_kernel<kQuantE4M3, true, VPT>, VPT)                     \
                                  : launch(silu_quant_kernel<kQuantE4M3, false, VPT>, VPT)))
-  // 28672 rows of 2048 in groups: 57 us with two vectors a thread, 60 with one or four.
+  // 28672 rows of 2048 in e4m3 groups: 59 us with two vectors a thread, 60.5 with one, 62.5 with four.
   const int vpt = vectors_for(nv, a.rows, sms, 2);
   return vpt == 1 ? MOE_PICK(1) : vpt == 2 ? MOE_PICK(2) : vpt == 4 ? MOE_PICK(4) : MOE_PICK(8);
 #undef MOE_PICK
