@@ -390,7 +390,7 @@ int moe_tail_selftest_wait_timeout(unsigned int limit_us, void* stream);
 
 /* Failure-detection test hook (no counterpart on the pages): the limit of
  * the operand-stage waits -- the tensor-core issuer of the GEMM kernels and
- * of the 8-bit product waiting for a stage of weights and tokens, the staged
+ * of the 8-bit and 4-bit products waiting for a stage of weights and tokens, the staged
  * expert-TP finalize kernel's
  * threads waiting for a stage of route rows -- for calls made after it
  * returns (process-wide), in nanoseconds (1: give up at the first such
@@ -454,6 +454,55 @@ int moe_tail_norm_quant(const void* x, const void* residual, const void* gamma, 
  */
 int moe_tail_silu_quant(const void* gate_up, const int32_t* used_rows, int rows, int I, int q_dtype,
                         int group, void* q, void* scale, void* stream);
+
+/*
+ * The norms after and before a block, fused with its gate and the residual.
+ * x is the block's output; per row t:
+ *   n = (x * rstd[t][0]) * (fp32(post_gamma) + gain_center)    (post_gamma NULL: n = x)
+ *   h = residual_scale * fp32(residual) + (token_gate[t] * fp32(channel_gate)) * n
+ *   residual_out = bf16(h)
+ *   y = bf16((h * rstd[t][1]) * (fp32(pre_gamma) + gain_center))   the next block's input
+ *   rstd[t][0] = 1 / sqrt(sum(x^2) * (1/H) + eps)              (post_gamma NULL: 1)
+ *   rstd[t][1] = 1 / sqrt(sum(h^2) * (1/H) + eps)
+ * All in FP32: the second norm is of h, not of its BF16 rounding.  A gate that
+ * is NULL is one.
+ *
+ *   x, residual, residual_out, y   BF16 [b][H]; residual_out may be x or
+ *                                  residual itself (in place)
+ *   post_gamma, pre_gamma, channel_gate   BF16 [H]
+ *   token_gate                     FP32 [b]
+ *   rstd                           FP32 [b][2], 8-byte aligned, or NULL; what
+ *                                  the gradient takes
+ * Limits: b <= 2^22, 8 <= H <= 32768, H % 8 == 0.
+ */
+int moe_tail_block_norm(const void* x, const void* residual, const void* post_gamma, const void* pre_gamma,
+                        const float* token_gate, const void* channel_gate, float residual_scale,
+                        float gain_center, float eps, int b, int H, void* residual_out, void* y, float* rstd,
+                        void* stream);
+
+/*
+ * The gradients of that, given d_y and d_residual_out (BF16 [b][H]; NULL:
+ * zeros), from the same x, residual, gammas and gates and the rstd it left.  h
+ * is formed again from x and residual, so those are what to keep.
+ *   d_x, d_residual   BF16 [b][H]; d_x may be d_y itself and d_residual
+ *                     d_residual_out
+ *   d_post_gamma, d_pre_gamma, d_channel_gate   FP32 [H] or NULL (not wanted),
+ *                     16-byte aligned: sums over the rows, in an order that
+ *                     depends on b, H and the GPU's number of SMs alone
+ *   d_token_gate      FP32 [b] or NULL
+ *   workspace         >= moe_tail_block_norm_grad_workspace_bytes(b, H) bytes,
+ *                     16-byte aligned; one for b rows serves fewer
+ * The gradient of a gamma or a gate that is NULL must be NULL.  b = 0 writes
+ * zeros to the sums over rows that are wanted.
+ * Limits: as moe_tail_block_norm.
+ */
+int moe_tail_block_norm_grad(const void* d_y, const void* d_residual_out, const void* x, const void* residual,
+                             const void* post_gamma, const void* pre_gamma, const float* token_gate,
+                             const void* channel_gate, const float* rstd, float residual_scale,
+                             float gain_center, int b, int H, void* d_x, void* d_residual,
+                             float* d_post_gamma, float* d_pre_gamma, float* d_token_gate,
+                             float* d_channel_gate, void* workspace, size_t workspace_bytes, void* stream);
+size_t moe_tail_block_norm_grad_workspace_bytes(int b, int H);
 
 /*
  * Routes sorted by expert.  Route r = t * K + k goes to expert_ids[t][k]; an
@@ -534,6 +583,51 @@ int moe_tail_expert_product(const void* x, const void* x_scale, const void* w, c
                             const int32_t* expert_offsets, int64_t rows, int num_experts, int N, int D,
                             void* out, void* workspace, size_t workspace_bytes, void* stream);
 size_t moe_tail_expert_product_workspace_bytes(int64_t rows, int num_experts, int N, int D);
+
+/*
+ * Product with 4-bit weights, a scale for each group of columns and for each
+ * channel, by expert or dense:
+ *   out[r][n] = bf16( (sum over k of fp32(x[r][k]) * W[e][n][k]) * channel_scale[e][n] )
+ *   W[e][n][k] = group_scale[e][n][k / group] * q[e][n][k],  q in [-8, 7]
+ * for the rows r of [expert_offsets[e], expert_offsets[e + 1]).  Rows of no
+ * expert are not written.  Every W is a BF16 number and every product exact in
+ * FP32; the sums are rounded as they grow, by at most (D + 256) * 2^-23 of the
+ * sum of their terms' magnitudes.
+ *   x          BF16 [rows][D]
+ *   w          q in 4 bits, [num_experts][N][64 * ceil(D / 128)] bytes: a
+ *              channel's columns in blocks of 128, sixteen 32-bit words
+ *              (little endian) each.  Word 4 t + i of a block (0 <= t, i < 4)
+ *              holds its columns 32 i + 8 t + c, 0 <= c < 8, as q + 8 in the
+ *              nibble (bits 4 j .. 4 j + 3) j = c / 2 for even c and
+ *              j = 4 + c / 2 (rounded down) for odd c.  Columns from D on may
+ *              hold anything.
+ *   group_scale    e4m3 [num_experts][N][pitch], pitch = ceil(D / group)
+ *              rounded up to a multiple of 4; scales from ceil(D / group) on
+ *              may hold anything
+ *   channel_scale  FP32 [num_experts][N]
+ *   expert_offsets device int32 [num_experts + 1], ascending within [0, rows]
+ *              (moe_tail_sort_routes), or NULL: one expert has every row
+ *   out        BF16 [rows][N]
+ * group is 32, 64 or 128.
+ * Limits: rows <= 2^22, num_experts <= 1024, 8 <= N <= 2^20, N % 8 == 0,
+ * 8 <= D <= 65536, D % 8 == 0.
+ */
+int moe_tail_expert_product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,
+                               const int32_t* expert_offsets, int64_t rows, int num_experts, int N, int D,
+                               int group, void* out, void* stream);
+
+/*
+ * The same with a weight of 2 I channels, I gate channels before I up
+ * channels, and the gated activation of the two in the same kernel:
+ *   out[r][i] = bf16( silu(p[r][i]) * p[r][I + i] ),  silu(g) = g / (1 + exp(-g))
+ * p the product above before its rounding (FP32 until the end).
+ *   w [num_experts][2 I][...], group_scale [num_experts][2 I][pitch],
+ *   channel_scale [num_experts][2 I], out BF16 [rows][I]
+ * Limits: as above with I for N.
+ */
+int moe_tail_gated_product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,
+                              const int32_t* expert_offsets, int64_t rows, int num_experts, int I, int D,
+                              int group, void* out, void* stream);
 
 #ifdef __cplusplus
 }

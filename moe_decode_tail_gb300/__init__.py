@@ -24,13 +24,16 @@ __all__ = [
     "FORM_LATENT_ONE_KERNEL", "moe_tail_set_stage_wait_limit", "moe_tail_up_project_shared_down",
     "moe_shared_down_persistent", "moe_tail_norm_quant", "moe_tail_silu_quant", "moe_tail_sort_routes",
     "moe_tail_sort_workspace_bytes", "moe_tail_dispatch_rows", "moe_tail_combine_rows", "moe_tail_combine_grad",
-    "moe_tail_expert_product", "moe_tail_expert_product_workspace_bytes",
+    "moe_tail_expert_product", "moe_tail_expert_product_workspace_bytes", "moe_tail_block_norm",
+    "moe_tail_block_norm_grad", "moe_tail_block_norm_grad_workspace_bytes", "moe_tail_expert_product_i4",
+    "moe_tail_gated_product_i4",
 ]
 
 OK, EINVAL, ECUDA, ENOTSUP = 0, 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 1 << 20  # MOE_TAIL_NOALLOC_SCRATCH_BYTES
 W_FP32, W_BF16 = 0, 1
 Q_DTYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}  # MOE_TAIL_Q_*: the types of 8-bit rows
+I4_GROUPS = (32, 64, 128)  # columns of a group of 4-bit weights
 QUANT_GROUP = 128  # columns of a group where a row has several scales
 WEIGHTS_STATIC = 1  # MOE_TAIL_WEIGHTS_STATIC
 INPUTS_READY = 2  # MOE_TAIL_INPUTS_READY
@@ -93,6 +96,12 @@ def lib() -> ctypes.CDLL:
         L.moe_tail_expert_product.argtypes = [P, P, P, P, P, i64, i32, i32, i32, P, P, sz, P]
         L.moe_tail_expert_product_workspace_bytes.argtypes = [i64, i32, i32, i32]
         L.moe_tail_expert_product_workspace_bytes.restype = sz
+        L.moe_tail_block_norm.argtypes = [P, P, P, P, P, P, f32, f32, f32, i32, i32, P, P, P, P]
+        L.moe_tail_block_norm_grad.argtypes = [P] * 9 + [f32, f32, i32, i32] + [P] * 7 + [sz, P]
+        L.moe_tail_block_norm_grad_workspace_bytes.argtypes = [i32, i32]
+        L.moe_tail_block_norm_grad_workspace_bytes.restype = sz
+        L.moe_tail_expert_product_i4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
+        L.moe_tail_gated_product_i4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
         for name in ("moe_tail_ep_finalize", "moe_tail_tp_finalize", "moe_tail_latent_up", "moe_shared_expert",
                      "moe_tail_norm_quant", "moe_tail_silu_quant", "moe_tail_sort_routes", "moe_tail_dispatch_rows",
                      "moe_tail_combine_rows", "moe_tail_combine_grad", "moe_tail_expert_product",
@@ -100,7 +109,8 @@ def lib() -> ctypes.CDLL:
                      "moe_tail_latent_norm", "moe_tail_up_project", "moe_shared_gate_up", "moe_shared_down",
                      "moe_tail_latent_up_flags", "moe_tail_ep_finalize_flags", "moe_tail_tp_finalize_flags",
                      "moe_tail_set_kernel_form", "moe_tail_set_stage_wait_limit",
-                     "moe_tail_up_project_shared_down", "moe_shared_down_persistent"):
+                     "moe_tail_up_project_shared_down", "moe_shared_down_persistent", "moe_tail_block_norm",
+                     "moe_tail_block_norm_grad", "moe_tail_expert_product_i4", "moe_tail_gated_product_i4"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -132,6 +142,15 @@ def _cuda(*ts):
     for t in ts:
         if t is not None and not (t.is_cuda and t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _cuda_here(*ts):
+    """Contiguous CUDA tensors of the current device, which is where a call launches its kernels."""
+    _cuda(*ts)
+    here = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device, cuda:{here}, got {t.device}")
 
 
 def _dims(name: str, t, n: int) -> tuple:
@@ -476,6 +495,70 @@ def moe_tail_silu_quant(gate_up, q, scale, *, used_rows=None, group=0, stream=No
     return q, scale
 
 
+def _rows_and_vectors(shape, rows, vectors) -> None:
+    """Named BF16 rows of one shape [b, H], and vectors [H] of a type; those that are None are left out."""
+    for name, t in rows.items():
+        if t is not None:
+            _like(name, t, torch.bfloat16, shape)
+    for name, (t, dtype, length) in vectors.items():
+        if t is not None:
+            _like(name, t, dtype, (length,))
+
+
+def moe_tail_block_norm(x, residual, post_gamma, pre_gamma, residual_out, y, *, token_gate=None, channel_gate=None, rstd=None,
+                        residual_scale=1.0, gain_center=1.0, eps=1e-6, stream=None):
+    """h = residual_scale * residual + token_gate * channel_gate * n into residual_out, n the RMS norm of x with gains
+    post_gamma + gain_center (post_gamma None: x itself), and the RMS norm of h with gains pre_gamma + gain_center into y:
+    x, residual, residual_out, y BF16 [b, H] (residual_out may be x or residual), gammas BF16 [H].  token_gate (FP32 [b])
+    and channel_gate (BF16 [H]) may each be None: ones.  rstd (FP32 [b, 2] or None) receives 1 / rms of x and of h, for
+    moe_tail_block_norm_grad.  Returns (residual_out, y)."""
+    shape = b, H = _dims("x", x, 2)
+    bf, f32 = torch.bfloat16, torch.float32
+    _rows_and_vectors(shape, {"x": x, "residual": residual, "residual_out": residual_out, "y": y},
+                      {"post_gamma": (post_gamma, bf, H), "pre_gamma": (pre_gamma, bf, H), "token_gate": (token_gate, f32, b),
+                       "channel_gate": (channel_gate, bf, H)})
+    if rstd is not None:
+        _like("rstd", rstd, f32, (b, 2))
+    _cuda_here(x, residual, post_gamma, pre_gamma, residual_out, y, token_gate, channel_gate, rstd)
+    _check("moe_tail_block_norm", lib().moe_tail_block_norm(
+        _p(x), _p(residual), _p(post_gamma), _p(pre_gamma), _p(token_gate), _p(channel_gate), residual_scale, gain_center, eps,
+        b, H, _p(residual_out), _p(y), _p(rstd), _stream(stream)))
+    return residual_out, y
+
+
+def moe_tail_block_norm_grad_workspace_bytes(b: int, H: int) -> int:
+    return int(lib().moe_tail_block_norm_grad_workspace_bytes(b, H))
+
+
+def moe_tail_block_norm_grad(d_y, d_residual_out, x, residual, post_gamma, pre_gamma, rstd, d_x, d_residual, workspace, *,
+                             token_gate=None, channel_gate=None, d_post_gamma=None, d_pre_gamma=None, d_token_gate=None,
+                             d_channel_gate=None, residual_scale=1.0, gain_center=1.0, stream=None):
+    """The gradients of moe_tail_block_norm given d_y and d_residual_out (BF16 [b, H]; d_residual_out may be None: zeros), its
+    inputs and the rstd it left: d_x and d_residual (BF16 [b, H]; they may be d_y and d_residual_out), and where they are
+    wanted d_post_gamma, d_pre_gamma and d_channel_gate (FP32 [H]) and d_token_gate (FP32 [b]).  workspace: a CUDA tensor of
+    at least moe_tail_block_norm_grad_workspace_bytes(b, H) bytes.  Returns (d_x, d_residual)."""
+    shape = b, H = _dims("d_y", d_y, 2)
+    bf, f32 = torch.bfloat16, torch.float32
+    for name, grad, of in (("d_post_gamma", d_post_gamma, post_gamma), ("d_token_gate", d_token_gate, token_gate),
+                           ("d_channel_gate", d_channel_gate, channel_gate)):
+        if grad is not None and of is None:
+            raise ValueError(f"{name} must be None where {name[2:]} is")
+    _rows_and_vectors(shape, {"d_y": d_y, "d_residual_out": d_residual_out, "x": x, "residual": residual, "d_x": d_x,
+                              "d_residual": d_residual},
+                      {"post_gamma": (post_gamma, bf, H), "pre_gamma": (pre_gamma, bf, H), "token_gate": (token_gate, f32, b),
+                       "channel_gate": (channel_gate, bf, H), "d_post_gamma": (d_post_gamma, f32, H),
+                       "d_pre_gamma": (d_pre_gamma, f32, H), "d_token_gate": (d_token_gate, f32, b),
+                       "d_channel_gate": (d_channel_gate, f32, H)})
+    _like("rstd", rstd, f32, (b, 2))
+    _cuda_here(d_y, d_residual_out, x, residual, post_gamma, pre_gamma, rstd, d_x, d_residual, workspace, token_gate,
+               channel_gate, d_post_gamma, d_pre_gamma, d_token_gate, d_channel_gate)
+    _check("moe_tail_block_norm_grad", lib().moe_tail_block_norm_grad(
+        _p(d_y), _p(d_residual_out), _p(x), _p(residual), _p(post_gamma), _p(pre_gamma), _p(token_gate), _p(channel_gate),
+        _p(rstd), residual_scale, gain_center, b, H, _p(d_x), _p(d_residual), _p(d_post_gamma), _p(d_pre_gamma),
+        _p(d_token_gate), _p(d_channel_gate), _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return d_x, d_residual
+
+
 def moe_tail_sort_workspace_bytes(b: int, K: int, num_experts: int) -> int:
     return int(lib().moe_tail_sort_workspace_bytes(b, K, num_experts))
 
@@ -587,6 +670,41 @@ def moe_tail_expert_product(x, x_scale, w, w_scale, out, workspace, *, expert_of
         _p(x), _p(x_scale), _p(w), _p(w_scale), _p(expert_offsets), rows, E, N, D, _p(out), _p(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
+
+
+def _product_i4(name, x, w, group_scale, channel_scale, out, group, expert_offsets, halves, stream):
+    rows, D = _dims("x", x, 2)
+    E, channels, _ = _dims("w", w, 3)
+    if group not in I4_GROUPS:
+        raise ValueError(f"group must be one of {I4_GROUPS}, got {group}")
+    if channels % halves:
+        raise ValueError(f"w must have an even number of channels (gate and up), got shape {tuple(w.shape)}")
+    _like("x", x, torch.bfloat16, (rows, D))
+    _like("w", w, torch.uint8, (E, channels, -(-D // 128) * 64))
+    _like("group_scale", group_scale, torch.float8_e4m3fn, (E, channels, -(-(-(-D // group)) // 4) * 4))
+    _like("channel_scale", channel_scale, torch.float32, (E, channels))
+    if expert_offsets is not None:
+        _like("expert_offsets", expert_offsets, torch.int32, (E + 1,))
+    _like("out", out, torch.bfloat16, (rows, channels // halves))
+    _cuda_here(x, w, group_scale, channel_scale, expert_offsets, out)
+    _check(name, getattr(lib(), name)(
+        _p(x), _p(w), _p(group_scale), _p(channel_scale), _p(expert_offsets), rows, E, channels // halves, D, group, _p(out),
+        _stream(stream)))
+    return out
+
+
+def moe_tail_expert_product_i4(x, w, group_scale, channel_scale, out, *, group, expert_offsets=None, stream=None) -> torch.Tensor:
+    """out (BF16 [rows, N]) = x (BF16 [rows, D]) times the transpose of each row's expert's 4-bit weight: w uint8
+    [num_experts, N, 64 * ceil(D / 128)] in the layout of include/moe_tail.h (expert_layer.quantise_groups makes it),
+    group_scale float8_e4m3fn [num_experts, N, ceil(D / group) up to a multiple of 4], channel_scale FP32 [num_experts, N];
+    group 32, 64 or 128; expert_offsets int32 [num_experts + 1] (moe_tail_sort_routes), or None with one expert."""
+    return _product_i4("moe_tail_expert_product_i4", x, w, group_scale, channel_scale, out, group, expert_offsets, 1, stream)
+
+
+def moe_tail_gated_product_i4(x, w, group_scale, channel_scale, out, *, group, expert_offsets=None, stream=None) -> torch.Tensor:
+    """out (BF16 [rows, I]) = silu(gate) * up in one kernel, gate and up the first and last I channels of that product
+    with a weight of 2 I channels (arguments as for moe_tail_expert_product_i4)."""
+    return _product_i4("moe_tail_gated_product_i4", x, w, group_scale, channel_scale, out, group, expert_offsets, 2, stream)
 
 
 def moe_tail_status_str(status: int) -> str:

@@ -59,6 +59,39 @@ struct SiluQuantArgs {
 };
 cudaError_t launch_silu_quant(const SiluQuantArgs& a, int kind, bool grouped, int sms, cudaStream_t stream);
 
+// ---- norms around a block (block_norm.cu) ----------------------------------------
+
+struct BlockNormArgs {
+  const uint16_t* x;             // BF16 [b][H]
+  const uint16_t* residual;      // BF16 [b][H]
+  const uint16_t* post_gamma;    // BF16 [H] or null: no norm after the block
+  const uint16_t* pre_gamma;     // BF16 [H]
+  const float* token_gate;       // [b] or null
+  const uint16_t* channel_gate;  // BF16 [H] or null
+  float residual_scale, gain_center, eps, rcpH;
+  int b, H;
+  uint16_t* residual_out;        // BF16 [b][H] (may be x or residual)
+  uint16_t* y;                   // BF16 [b][H]
+  float* rstd;                   // [b][2] or null
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, int sms, cudaStream_t stream);
+
+struct BlockNormGradArgs {
+  const uint16_t *d_y, *d_residual_out;  // BF16 [b][H]; d_residual_out may be null
+  const uint16_t *x, *residual, *post_gamma, *pre_gamma;
+  const float* token_gate;
+  const uint16_t* channel_gate;
+  const float* rstd;
+  float residual_scale, gain_center, rcpH;
+  int b, H;
+  uint16_t *d_x, *d_residual;            // BF16 [b][H] (may be d_y and d_residual_out)
+  float *d_post_gamma, *d_pre_gamma, *d_channel_gate;  // [H] or null
+  float* d_token_gate;                   // [b] or null
+  float* partial;                        // workspace [row sets][3][H]
+};
+cudaError_t launch_block_norm_grad(const BlockNormGradArgs& a, int sms, cudaStream_t stream);
+size_t block_norm_grad_workspace(int b, int H);
+
 // ---- routes (routes.cu) ----------------------------------------------------------
 
 int sort_blocks(int routes);  // thread blocks of a sort, each with a row of counts in the workspace
@@ -120,5 +153,29 @@ size_t expert_product_workspace(int64_t R, int E, int N, int D);
 int product_rows_of_tile(int64_t R, int E);
 // Read and clear the product's device error word (synchronises).
 cudaError_t take_product_error(unsigned* bits);
+
+// ---- 4-bit product (product_i4.cu) -----------------------------------------------
+
+struct ProductI4Args {
+  const uint8_t* group_scale;  // e4m3 [E][channels][pitch]; channels: N, gated 2 N
+  const float* channel_scale;  // [E][channels]
+  const int32_t* offsets;      // [E + 1] or null (E = 1: all rows)
+  uint16_t* out;               // BF16 [R][N]
+  int64_t R;
+  int E, N, D, group;
+  bool gated;
+};
+struct ProductI4Plan {
+  int rows;          // of a tile
+  int splits;        // warps along the reduction
+  int box_channels;  // channels of the result of a tile
+};
+ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sms);
+// map_w: w as [E][channels][64 ceil(D / 128)] bytes, boxes of box_channels x 64 bytes; gated as [E][2][N][...], boxes of
+// 2 x box_channels x 64; no swizzle.  map_x: x [R][D] in boxes of plan.rows x 64 with the 128-byte swizzle.  Zeros out of
+// range.
+cudaError_t launch_product_i4(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
+                              const CUtensorMap& map_x, int sms, cudaStream_t stream);
+cudaError_t take_product_i4_error(unsigned* bits);
 
 }  // namespace moetail

@@ -113,6 +113,105 @@ MOE_API int moe_tail_silu_quant(const void* gate_up, const int32_t* used_rows, i
   return finish(moetail::launch_silu_quant(a, q_dtype, group != 0, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
+// ============================================================================ norms around a block
+
+MOE_API int moe_tail_block_norm(const void* x, const void* residual, const void* post_gamma, const void* pre_gamma,
+                                const float* token_gate, const void* channel_gate, float residual_scale,
+                                float gain_center, float eps, int b, int H, void* residual_out, void* y, float* rstd,
+                                void* stream) {
+  if (b < 0 || b > kMaxRows || !width_ok(H)) return MOE_TAIL_EINVAL;
+  if (b == 0) return MOE_TAIL_OK;
+  const size_t n = (size_t)b * H, row = 2 * (size_t)H;
+  // the new residual may take x's or the residual's own place: each element is read before it is written
+  const bool in_x = residual_out && residual_out == x, in_residual = residual_out && residual_out == residual;
+  const Operand in[] = {{in_x ? nullptr : x, 2 * n, 16, in_x},
+                        {in_residual ? nullptr : residual, 2 * n, 16, in_residual},
+                        {post_gamma, row, 16, true},
+                        {pre_gamma, row, 16, false},
+                        {token_gate, 4 * (size_t)b, 4, true},
+                        {channel_gate, row, 16, true}};
+  const Operand out[] = {{residual_out, 2 * n, 16, false}, {y, 2 * n, 16, false}, {rstd, 8 * (size_t)b, 8, true}};
+  if (!operands_ok(in, out)) return MOE_TAIL_EINVAL;
+  moetail::BlockNormArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.post_gamma = static_cast<const uint16_t*>(post_gamma);
+  a.pre_gamma = static_cast<const uint16_t*>(pre_gamma);
+  a.token_gate = token_gate;
+  a.channel_gate = static_cast<const uint16_t*>(channel_gate);
+  a.residual_scale = residual_scale;
+  a.gain_center = gain_center;
+  a.eps = eps;
+  a.rcpH = (float)(1.0 / (double)H);
+  a.b = b;
+  a.H = H;
+  a.residual_out = static_cast<uint16_t*>(residual_out);
+  a.y = static_cast<uint16_t*>(y);
+  a.rstd = rstd;
+  return finish(moetail::launch_block_norm(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API size_t moe_tail_block_norm_grad_workspace_bytes(int b, int H) {
+  if (b < 0 || b > kMaxRows || !width_ok(H)) return 0;
+  return round256(moetail::block_norm_grad_workspace(b < 1 ? 1 : b, H));
+}
+
+MOE_API int moe_tail_block_norm_grad(const void* d_y, const void* d_residual_out, const void* x, const void* residual,
+                                     const void* post_gamma, const void* pre_gamma, const float* token_gate,
+                                     const void* channel_gate, const float* rstd, float residual_scale,
+                                     float gain_center, int b, int H, void* d_x, void* d_residual, float* d_post_gamma,
+                                     float* d_pre_gamma, float* d_token_gate, float* d_channel_gate, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (b < 0 || b > kMaxRows || !width_ok(H)) return MOE_TAIL_EINVAL;
+  // a gradient of what is not there
+  if ((d_post_gamma && !post_gamma) || (d_token_gate && !token_gate) || (d_channel_gate && !channel_gate))
+    return MOE_TAIL_EINVAL;
+  const size_t n = (size_t)b * H, row = 2 * (size_t)H, tokens = 4 * (size_t)b;
+  // d_x may take d_y's place and d_residual d_residual_out's: each element is read before it is written
+  const bool in_y = d_x && d_x == d_y, in_residual = d_residual && d_residual == d_residual_out;
+  const Operand in[] = {{in_y ? nullptr : d_y, 2 * n, 16, in_y},
+                        {in_residual ? nullptr : d_residual_out, 2 * n, 16, true},
+                        {x, 2 * n, 16, false},
+                        {residual, 2 * n, 16, false},
+                        {post_gamma, row, 16, true},
+                        {pre_gamma, row, 16, false},
+                        {token_gate, tokens, 4, true},
+                        {channel_gate, row, 16, true},
+                        {rstd, 2 * tokens, 8, false}};
+  const Operand out[] = {{d_x, 2 * n, 16, false},
+                         {d_residual, 2 * n, 16, false},
+                         {d_post_gamma, 4 * (size_t)H, 16, true},
+                         {d_pre_gamma, 4 * (size_t)H, 16, true},
+                         {d_token_gate, tokens, 4, true},
+                         {d_channel_gate, 4 * (size_t)H, 16, true},
+                         {workspace, workspace_bytes, 16, false}};
+  if (workspace_bytes < moe_tail_block_norm_grad_workspace_bytes(b, H) || !operands_ok(in, out)) return MOE_TAIL_EINVAL;
+  if (b == 0 && !d_post_gamma && !d_pre_gamma && !d_channel_gate) return MOE_TAIL_OK;
+  moetail::BlockNormGradArgs a;
+  a.d_y = static_cast<const uint16_t*>(d_y);
+  a.d_residual_out = static_cast<const uint16_t*>(d_residual_out);
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.post_gamma = static_cast<const uint16_t*>(post_gamma);
+  a.pre_gamma = static_cast<const uint16_t*>(pre_gamma);
+  a.token_gate = token_gate;
+  a.channel_gate = static_cast<const uint16_t*>(channel_gate);
+  a.rstd = rstd;
+  a.residual_scale = residual_scale;
+  a.gain_center = gain_center;
+  a.rcpH = (float)(1.0 / (double)H);
+  a.b = b;
+  a.H = H;
+  a.d_x = static_cast<uint16_t*>(d_x);
+  a.d_residual = static_cast<uint16_t*>(d_residual);
+  a.d_post_gamma = d_post_gamma;
+  a.d_pre_gamma = d_pre_gamma;
+  a.d_channel_gate = d_channel_gate;
+  a.d_token_gate = d_token_gate;
+  a.partial = static_cast<float*>(workspace);
+  return finish(moetail::launch_block_norm_grad(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
 // ============================================================================ routes
 
 MOE_API size_t moe_tail_sort_workspace_bytes(int b, int K, int num_experts) {
@@ -289,4 +388,76 @@ MOE_API int moe_tail_expert_product(const void* x, const void* x_scale, const vo
     return MOE_TAIL_ECUDA;
   return finish(
       moetail::launch_expert_product(a, map_w, map_x, workspace, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+// ============================================================================ 4-bit product
+
+namespace {
+
+bool i4_sizes_ok(int64_t R, int E, int N, int D, int group) {
+  return R >= 0 && R <= kMaxRows && E >= 1 && E <= kMaxExperts && N >= 8 && N <= kMaxN && N % 8 == 0 && D >= 8 &&
+         D <= kMaxD && D % 8 == 0 && (group == 32 || group == 64 || group == 128);
+}
+
+bool encode_i4_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const void* x, int64_t R, int E, int N, int D,
+                    bool gated, const moetail::ProductI4Plan& plan) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t bytes = 64 * (cuuint64_t)((D + 127) / 128), channels = (cuuint64_t)N, experts = (cuuint64_t)E;
+  const cuuint32_t box = (cuuint32_t)plan.box_channels, ones[4] = {1, 1, 1, 1};
+  const cuuint64_t wd3[3] = {bytes, channels, experts}, wst3[2] = {bytes, bytes * channels};
+  const cuuint64_t wd4[4] = {bytes, channels, 2, experts}, wst4[3] = {bytes, bytes * channels, 2 * bytes * channels};
+  const cuuint32_t wb3[3] = {64, box, 1}, wb4[4] = {64, box, 2, 1};
+  const cuuint64_t xd[2] = {(cuuint64_t)D, (cuuint64_t)R}, xst[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t xb[2] = {64, (cuuint32_t)plan.rows};
+  return enc(map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 4 : 3, const_cast<void*>(w), gated ? wd4 : wd3,
+             gated ? wst4 : wst3, gated ? wb4 : wb3, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         enc(map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), xd, xst, xb, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,
+               const int32_t* expert_offsets, int64_t rows, int num_experts, int N, int D, int group, bool gated, void* out,
+               void* stream) {
+  if (!i4_sizes_ok(rows, num_experts, N, D, group) || (!expert_offsets && num_experts != 1)) return MOE_TAIL_EINVAL;
+  if (rows == 0) return MOE_TAIL_OK;
+  const size_t channels = (size_t)num_experts * N * (gated ? 2 : 1), pitch = ((D + group - 1) / group + 3) / 4 * 4;
+  const Operand in[] = {{x, (size_t)rows * D * 2, 16, false},
+                        {w, channels * 64 * ((D + 127) / 128), 16, false},
+                        {group_scale, channels * pitch, 4, false},
+                        {channel_scale, 4 * channels, 4, false},
+                        {expert_offsets, 4 * ((size_t)num_experts + 1), 4, true}};
+  const Operand outs[] = {{out, (size_t)rows * N * 2, 16, false}};
+  if (!operands_ok(in, outs)) return MOE_TAIL_EINVAL;
+  moetail::ProductI4Args a;
+  a.group_scale = static_cast<const uint8_t*>(group_scale);
+  a.channel_scale = channel_scale;
+  a.offsets = expert_offsets;
+  a.out = static_cast<uint16_t*>(out);
+  a.R = rows;
+  a.E = num_experts;
+  a.N = N;
+  a.D = D;
+  a.group = group;
+  a.gated = gated;
+  const moetail::ProductI4Plan plan = moetail::product_i4_plan(rows, num_experts, N, D, gated, device_sms());
+  CUtensorMap map_w, map_x;
+  if (!encode_i4_maps(&map_w, &map_x, w, x, rows, num_experts, N, D, gated, plan)) return MOE_TAIL_ECUDA;
+  return finish(moetail::launch_product_i4(a, plan, map_w, map_x, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+MOE_API int moe_tail_expert_product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,
+                                       const int32_t* expert_offsets, int64_t rows, int num_experts, int N, int D,
+                                       int group, void* out, void* stream) {
+  return product_i4(x, w, group_scale, channel_scale, expert_offsets, rows, num_experts, N, D, group, false, out, stream);
+}
+
+MOE_API int moe_tail_gated_product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,
+                                      const int32_t* expert_offsets, int64_t rows, int num_experts, int I, int D, int group,
+                                      void* out, void* stream) {
+  return product_i4(x, w, group_scale, channel_scale, expert_offsets, rows, num_experts, I, D, group, true, out, stream);
 }
