@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libmoetail.so")
 TRACE_LIB = os.path.join(BUILD, "libmoetail_trace.so")  # the same kernels with the per-CTA trace
 FLOOR_LIB = os.path.join(BUILD, "libmoetail_floor.so")  # latency-floor kernels (measurement only)
 SOURCES = ["finalize.cu", "decode_gemm.cu", "moe_tail_api.cu", "noalloc.cu", "row_quant.cu", "routes.cu", "expert_product.cu",
-           "layer_api.cu", "block_norm.cu", "product_i4.cu"]
+           "layer_api.cu", "block_norm.cu", "product_i4.cu", "product_i4_tiles.cu"]
 FLOOR_SOURCES = ["floor.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

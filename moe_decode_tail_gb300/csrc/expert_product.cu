@@ -117,29 +117,7 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const int8_t* x, uint1
 __device__ __forceinline__ uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
-}
-// A barrier over the four warps of an epilogue set.
-__device__ __forceinline__ void set_bar(int set) {
-  together();
-  asm volatile("bar.sync %0, 128;" ::"r"(2 + set) : "memory");
-}
-// Barrier 1 over `threads`; whether `ok` holds in all of them.
-template <int THREADS>
-__device__ __forceinline__ bool all_of(bool ok) {
-  uint32_t all;
-  together();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"((uint32_t)ok), "n"(THREADS)
-      : "memory");
-  return all != 0;
-}
+
 // ---- the product ----------------------------------------------------------------------
 
 // A part: reduction blocks [k0, k0 + blocks) of 128 channels from m0 by rows [r0, r0 + rows) of expert e.

@@ -165,17 +165,23 @@ struct ProductI4Args {
   int E, N, D, group;
   bool gated;
 };
+// Which kernel a call takes and how its operands are read.
 struct ProductI4Plan {
+  bool tiles;        // tiles on the tensor cores (product_i4_tiles.cu); else warps that multiply (product_i4.cu)
   int rows;          // of a tile
-  int splits;        // warps along the reduction
-  int box_channels;  // channels of the result of a tile
+  int splits;        // warps along the reduction (no tiles)
+  int box_channels;  // of one half of a gated weight, or of a plain one, in a box of w
+  int box_rows;      // in a box of x
 };
 ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sms);
 // map_w: w as [E][channels][64 ceil(D / 128)] bytes, boxes of box_channels x 64 bytes; gated as [E][2][N][...], boxes of
-// 2 x box_channels x 64; no swizzle.  map_x: x [R][D] in boxes of plan.rows x 64 with the 128-byte swizzle.  Zeros out of
-// range.
+// 2 x box_channels x 64; with tiles the 64-byte swizzle, else none.  map_x: x [R][D] in boxes of box_rows x 64 with the
+// 128-byte swizzle.  Zeros out of range.
 cudaError_t launch_product_i4(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
                               const CUtensorMap& map_x, int sms, cudaStream_t stream);
+cudaError_t launch_product_i4_tiles(const ProductI4Args& p, int rows, const CUtensorMap& map_w, const CUtensorMap& map_x,
+                                    int sms, cudaStream_t stream);
+cudaError_t take_product_i4_tiles_error(unsigned* bits);
 cudaError_t take_product_i4_error(unsigned* bits);
 
 }  // namespace moetail

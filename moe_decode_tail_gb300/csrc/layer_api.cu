@@ -409,10 +409,10 @@ bool encode_i4_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const
   const cuuint64_t wd4[4] = {bytes, channels, 2, experts}, wst4[3] = {bytes, bytes * channels, 2 * bytes * channels};
   const cuuint32_t wb3[3] = {64, box, 1}, wb4[4] = {64, box, 2, 1};
   const cuuint64_t xd[2] = {(cuuint64_t)D, (cuuint64_t)R}, xst[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t xb[2] = {64, (cuuint32_t)plan.rows};
+  const cuuint32_t xb[2] = {64, (cuuint32_t)plan.box_rows};
   return enc(map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 4 : 3, const_cast<void*>(w), gated ? wd4 : wd3,
-             gated ? wst4 : wst3, gated ? wb4 : wb3, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+             gated ? wst4 : wst3, gated ? wb4 : wb3, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             plan.tiles ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
          enc(map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), xd, xst, xb, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -14,7 +14,7 @@ __device__ __forceinline__ void together() { __syncwarp(); }
 
 // D[tmem_d] (+)= A[tmem_a] * B[bdesc], operands of idesc's type, FP32 sums.
 __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
+                                       uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -48,6 +48,29 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+// A barrier over the four warps of an epilogue set.
+__device__ __forceinline__ void set_bar(int set) {
+  together();
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + set) : "memory");
+}
+// Barrier 1 over `threads`; whether `ok` holds in all of them.
+template <int THREADS>
+__device__ __forceinline__ bool all_of(bool ok) {
+  uint32_t all;
+  together();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "n"(THREADS)
+      : "memory");
+  return all != 0;
+}
 // By a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           unsigned long long limit_ns = kWaitLimitNs) {

@@ -5,12 +5,9 @@
 //
 // x BF16, q in [-8, 7], gs e4m3, cs FP32.  A BF16 times a q is exact in FP32, and a q times a gs (three and four
 // significant bits) is exact in BF16, so the tensor cores' products are exact either way and only their FP32 sums round.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
 #include "kernels.h"
 #include "layer.h"
-#include "product.cuh"
+#include "product_i4.cuh"
 
 namespace moetail {
 
@@ -30,48 +27,23 @@ struct Args {
   int groups, pitch;           // scales of a channel, and their distance to the next channel's
   int stages;
   int splits;                  // warps along the reduction
+  int depth;                   // blocks of a warp in a stage
   unsigned long long stage_wait_ns;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int u,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 // D = A (16 channels x 16 columns) * B (16 columns x 8 rows) + C, BF16, FP32 sums.
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                            const float (&c)[4]) {
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with C = 0.
+__device__ __forceinline__ void mma_16x8x16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-
-// Columns c = 0 .. 7 of a stored word as four pairs of BF16: a nibble q + 8 under the exponent of 128 is the BF16
-// number 136 + q, and the subtraction is exact.
-__device__ __forceinline__ void int4x8_to_bf16(uint32_t word, uint32_t (&pair)[4]) {
-  const __nv_bfloat162 base = __bfloat162bfloat162(__ushort_as_bfloat16((unsigned short)0x4308));  // 136
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), base);
-    pair[i] = *reinterpret_cast<const uint32_t*>(&q);
-  }
-}
-
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(byte & 0xffu), __NV_E4M3)));
-}
-
-// silu(g) * up.  With e = exp(-|g| / 2) the divisor is 1 + e^2; for g < 0 the fraction is multiplied by e^2 above and
-// below, one e with each factor, so that nothing leaves FP32's range before the result does.
-__device__ __forceinline__ float silu_times(float g, float up) {
-  const float e = expf(-0.5f * fabsf(g)), p = g < 0.0f ? e : 1.0f;
-  return __fdividef((g * p) * (up * p), fmaf(e, e, 1.0f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // ---- few rows for an expert ------------------------------------------------------------------------------------------
@@ -100,7 +72,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
   const int across = kWarps / a.splits;         // warps along the channels
-  const int stage_bytes = kWarps * kWeightBlock + a.splits * kXBlock;
+  const int step_blocks = a.splits * a.depth;   // of a stage; a warp has every splits-th of them
+  const int weights_bytes = a.depth * kWarps * kWeightBlock, stage_bytes = weights_bytes + step_blocks * kXBlock;
   uint32_t at = base + (uint32_t)(a.stages * stage_bytes);
   const uint32_t red = at;
   float* s_red = reinterpret_cast<float*>(base_ptr + (red - base));  // [warps][8 rows][kPadded]
@@ -155,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
     if (!*abort_ptr) raise_error(bit);
     *abort_ptr = 1;
   };
-  const int steps = (a.blocks + a.splits - 1) / a.splits;
+  const int steps = (a.blocks + step_blocks - 1) / step_blocks;
 
   if (warp == kWarps) {
     // ---------------- copies ----------------
@@ -171,12 +144,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
           ok = false;
           break;
         }
-        const int here = min(a.splits, a.blocks - s * a.splits);  // blocks of this step
-        const uint32_t bar = full + 8 * ring.slot, w = base + ring.slot * stage_bytes, x = w + kWarps * kWeightBlock;
+        const int here = min(step_blocks, a.blocks - s * step_blocks);  // blocks of this step
+        const uint32_t bar = full + 8 * ring.slot, w = base + ring.slot * stage_bytes, x = w + weights_bytes;
         if (elect_one()) {
           mbar_expect_tx(bar, (uint32_t)(here * (across * kWeightBlock + kXBlock)));
           for (int k = 0; k < here; ++k) {
-            const int block = s * a.splits + k;
+            const int block = s * step_blocks + k;
             if (GATED) tma_load_4d(w + k * across * kWeightBlock, &map_w, bar, 64 * block, q.n0, 0, q.e, once);
             else tma_load_3d(w + k * across * kWeightBlock, &map_w, bar, 64 * block, q.n0, q.e, once);
             tma_load_2d(x + k * kXBlock, &map_x, bar, 128 * block, q.r0, keep);
@@ -209,38 +182,54 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
     channel0[j][0] = local[j][0];
     channel0[j][1] = local[j][0] + (GATED ? a.N : 8);
   }
-  // the scales of a block for the lane's channels, a byte for each group
-  auto load_scales = [&](const Tile& q, int block, uint32_t (&s)[2][2]) {
+  // Where the lane's channels' scales begin.  Channels past the last read the last one's.
+  const uint8_t* scale_base = nullptr;
+  uint32_t scale_at[2][2];
+  auto scales_of = [&](const Tile& q) {
+    scale_base = a.group_scale + (int64_t)q.e * channels * a.pitch;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        s[j][h] = 0;
-        if (block >= a.blocks || q.n0 + (GATED ? channel0[j][0] : channel0[j][h]) >= a.N) continue;
-        const uint8_t* p = a.group_scale + ((int64_t)q.e * channels + q.n0 + channel0[j][h]) * a.pitch + block * kPer;
-        s[j][h] = kPer == 1 ? __ldg(p) : kPer == 2 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : __ldg(reinterpret_cast<const uint32_t*>(p));
-        const int left = a.groups - block * kPer;  // behind the last group may stand anything
-        if (left < kPer) s[j][h] &= (1u << (8 * left)) - 1u;
+        const int past = GATED && h ? a.N : 0;
+        scale_at[j][h] = (uint32_t)(min(q.n0 + channel0[j][h] - past, a.N - 1) + past) * (uint32_t)a.pitch;
       }
   };
-  Ring ring;
-  bool ok = true;
-  Tile q, next;
-  uint32_t ahead[2][2];
-  int64_t i = blockIdx.x;
-  bool more = tile_at(i, q);
-  if (more) load_scales(q, split, ahead);
-  while (more) {
-    i += gridDim.x;
-    more = tile_at(i, next);
-    float cs[2][2];
+  // Four of the scales of each: word i of them; what stands behind the last group counts as zero.
+  auto load_scales = [&](int i, uint32_t (&s)[2][2]) {
+    const int left = a.groups - 4 * i;
+    if (left <= 0) return;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        cs[j][h] = q.n0 + (GATED ? channel0[j][0] : channel0[j][h]) < a.N
-                       ? __ldg(a.channel_scale + (int64_t)q.e * channels + q.n0 + channel0[j][h])
-                       : 0.0f;
+        s[j][h] = __ldg(reinterpret_cast<const uint32_t*>(scale_base + (scale_at[j][h] + 4u * i)));
+    if (left < 4) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[j][h] &= (1u << (8 * left)) - 1u;
+    }
+  };
+  const uint32_t w_lane = base + split * across * kWeightBlock + local[0][0] * 64 + 16 * t;
+  const uint32_t w_half = (local[0][1] - local[0][0]) * 64;  // from a lane's channel in the upper half of A's rows to the lower
+  const uint32_t x_lane = base + weights_bytes + split * kXBlock + x_row * 128;
+  const uint32_t x_unit[2] = {x_lane + ((t ^ x_row) << 4), x_lane + (((4 + t) ^ x_row) << 4)};
+  const Factors factors = unscaled();
+  int slot = 0;
+  uint32_t parity = 0, slot_at = 0;
+  bool ok = true;
+  Tile q, next;
+  uint32_t scales[2][2], ahead[2][2];  // of the block at hand, and the words after them
+  int64_t i = blockIdx.x;
+  bool more = tile_at(i, q);
+  if (more) {
+    scales_of(q);
+    load_scales(split * kPer / 4, ahead);
+  }
+  while (more) {
+    i += gridDim.x;
+    more = tile_at(i, next);
     const int row_groups = (q.rows + 7) >> 3;
     float acc[2][NT][4];
 #pragma unroll
@@ -249,66 +238,88 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[j][n][c] = 0.0f;
-    for (int s = 0; s < steps; ++s, ring.step(a.stages)) {
-      const int block = s * a.splits + split;
-      uint32_t scales[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) scales[j][h] = ahead[j][h];
-      if (s + 1 < steps) load_scales(q, block + a.splits, ahead);
-      else if (more) load_scales(next, split, ahead);
-      if (ok && !warp_wait(full + 8 * ring.slot, ring.parity, abort_ptr, limit)) {
+    int word = -1;
+    for (int block = split; block - split < a.blocks;) {
+      if (ok && !warp_wait(full + 8 * slot, parity, abort_ptr, limit)) {
         if (lane == 0) give_up(kErrWaitFull);
         ok = false;
       }
-      if (!ok) continue;  // the tiles are walked to the end: the warps meet at barriers
-      if (block < a.blocks) {
-        const uint32_t w = base + ring.slot * stage_bytes + split * across * kWeightBlock;
-        const uint32_t x = base + ring.slot * stage_bytes + kWarps * kWeightBlock + split * kXBlock;
-        uint4 words[2][2];
+#pragma unroll 1
+      for (int k = 0; k < a.depth; ++k, block += a.splits) {
+        if (!ok || block >= a.blocks) continue;  // the tiles are walked to the end: the warps meet at barriers
+        if (block * kPer / 4 != word) {
+          word = block * kPer / 4;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) words[j][h] = ld_shared_v4(w + local[j][h] * 64 + 16 * t);
-        float sum[2][NT][4];
+            for (int h = 0; h < 2; ++h) scales[j][h] = ahead[j][h];
+          // the warp's next block whose scales are in another word
+          const int after = a.splits * kPer >= 4 ? block + a.splits : (word + 1) * (4 / kPer) + split;
+          if (after < a.blocks) {
+            load_scales(after * kPer / 4, ahead);
+          } else if (more) {
+            scales_of(next);
+            load_scales(split * kPer / 4, ahead);
+          }
+        }
+        const uint32_t w = w_lane + slot_at + k * (kWarps * kWeightBlock), x = slot_at + k * a.splits * kXBlock;
+        const int first_byte = kPer == 4 ? 0 : 8 * (block * kPer & 3);
+        uint4 rows[NT][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 32 columns
-          uint4 rows[NT];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < row_groups)
-              rows[n] = ld_shared_v4(x + (c >> 1) * (kXBlock / 2) + (8 * n + x_row) * 128 + (((4 * (c & 1) + t) ^ x_row) << 4));
-          const bool first = (32 * c) % GROUP == 0, last = (32 * c + 32) % GROUP == 0;
+          for (int c = 0; c < 4; ++c)
+            if (NT == 1 || n < row_groups) rows[n][c] = ld_shared_v4(x_unit[c & 1] + x + (c >> 1) * (kXBlock / 2) + n * 1024);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t lo[4], hi[4];
-            const uint32_t wl = c == 0 ? words[j][0].x : c == 1 ? words[j][0].y : c == 2 ? words[j][0].z : words[j][0].w;
-            const uint32_t wh = c == 0 ? words[j][1].x : c == 1 ? words[j][1].y : c == 2 ? words[j][1].z : words[j][1].w;
-            int4x8_to_bf16(wl, lo);
-            int4x8_to_bf16(wh, hi);
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-            const float sl = e4m3_value(scales[j][0] >> (8 * (c / (4 / kPer)))), sh = e4m3_value(scales[j][1] >> (8 * (c / (4 / kPer))));
+        for (int j = 0; j < 2; ++j) {
+          const uint4 wl = ld_shared_v4(w + j * (GATED ? 512 : 1024)), wh = ld_shared_v4(w + w_half + j * (GATED ? 512 : 1024));
+          float sum[NT][4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 32 columns
+            uint32_t l[4], h[4];
+            int4x8_to_bf16(c == 0 ? wl.x : c == 1 ? wl.y : c == 2 ? wl.z : wl.w, factors, l);
+            int4x8_to_bf16(c == 0 ? wh.x : c == 1 ? wh.y : c == 2 ? wh.z : wh.w, factors, h);
+            const uint32_t a0[4] = {l[0], h[0], l[1], h[1]}, a1[4] = {l[2], h[2], l[3], h[3]};
+            const bool last = (32 * c + 32) % GROUP == 0;  // of a group
+            const int shift = first_byte + 8 * (32 * c / GROUP);
+            const float sl = e4m3_value(scales[j][0] >> shift), sh = e4m3_value(scales[j][1] >> shift);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (n >= row_groups) continue;
-              const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              if (first) mma_16x8x16(sum[j][n], a0, rows[n].x, rows[n].y, zero);
-              else mma_16x8x16(sum[j][n], a0, rows[n].x, rows[n].y, sum[j][n]);
-              mma_16x8x16(sum[j][n], a1, rows[n].z, rows[n].w, sum[j][n]);
+              if (NT > 1 && n >= row_groups) continue;
+              if (32 * c % GROUP == 0) mma_16x8x16_first(sum[n], a0, rows[n][c].x, rows[n][c].y);
+              else mma_16x8x16(sum[n], a0, rows[n][c].x, rows[n][c].y);
+              mma_16x8x16(sum[n], a1, rows[n][c].z, rows[n][c].w);
               if (last) {
-                acc[j][n][0] += sl * sum[j][n][0];
-                acc[j][n][1] += sl * sum[j][n][1];
-                acc[j][n][2] += sh * sum[j][n][2];
-                acc[j][n][3] += sh * sum[j][n][3];
+                acc[j][n][0] += sl * sum[n][0];
+                acc[j][n][1] += sl * sum[n][1];
+                acc[j][n][2] += sh * sum[n][2];
+                acc[j][n][3] += sh * sum[n][3];
               }
             }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * ring.slot);  // its products have taken what the loads brought
+      if (ok && lane == 0) mbar_arrive(empty + 8 * slot);  // its products have taken what the loads brought
+      slot_at += stage_bytes;
+      if (++slot == a.stages) {
+        slot = 0;
+        slot_at = 0;
+        parity ^= 1u;
+      }
     }
+    if (word < 0 && more) {  // no block for this warp
+      scales_of(next);
+      load_scales(split * kPer / 4, ahead);
+    }
+    float cs[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        cs[j][h] = q.n0 + (GATED ? channel0[j][0] : channel0[j][h]) < a.N
+                       ? kUnscaled * __ldg(a.channel_scale + (int64_t)q.e * channels + q.n0 + channel0[j][h])
+                       : 0.0f;
     // Eight rows at a time: the warps' sums to shared memory, those along the reduction added in their order, whole lines
     // of 16 bytes to the result.
 #pragma unroll
@@ -357,12 +368,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
 
 // ---- host --------------------------------------------------------------------------------------------------------------
 
-// Rows of a tile: those of one expert, else twice an expert's average share, so that an uneven batch still has one row
-// tile for most experts.
-int rows_of_tile(int64_t R, int E) {
-  const int64_t want = E == 1 ? R : 2 * ((R + E - 1) / E);
-  return want <= 8 ? 8 : want <= 16 ? 16 : 32;
-}
+constexpr int kFewRows = 8;
+
+// Rows of a tile: all of them where one expert has few, else twice an expert's average share, so that an uneven batch still
+// has one row tile for most experts.
+int64_t rows_wanted(int64_t R, int E) { return E == 1 ? R : 2 * ((R + E - 1) / E); }
 
 // Warps along the reduction: as few as leave every thread block at least three tiles.
 int splits_of(int64_t R, int E, int N, int blocks, bool gated, int rows, int grid) {
@@ -378,9 +388,19 @@ int splits_of(int64_t R, int E, int N, int blocks, bool gated, int rows, int gri
 
 ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sms) {
   ProductI4Plan p;
-  p.rows = rows_of_tile(R, E);
-  p.splits = splits_of(R, E, N, (D + 127) / 128, gated, p.rows, blocks_per_sm(p.rows / 8) * sms);
-  p.box_channels = (gated ? 16 : kWarpTile) * (kWarps / p.splits);
+  const int64_t want = rows_wanted(R, E);
+  p.tiles = want > kFewRows;
+  if (p.tiles) {
+    p.rows = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 256 ? 128 : 256;
+    p.splits = 0;
+    p.box_channels = gated ? 16 : 128;
+    p.box_rows = p.rows < 64 ? p.rows : 64;
+  } else {
+    p.rows = want <= 8 ? 8 : want <= 16 ? 16 : 32;
+    p.splits = splits_of(R, E, N, (D + 127) / 128, gated, p.rows, blocks_per_sm(p.rows / 8) * sms);
+    p.box_channels = (gated ? 16 : kWarpTile) * (kWarps / p.splits);
+    p.box_rows = p.rows;
+  }
   return p;
 }
 
@@ -402,8 +422,9 @@ cudaError_t launch_few(const ProductI4Args& p, const ProductI4Plan& plan, const 
   a.groups = (p.D + GROUP - 1) / GROUP;
   a.pitch = (a.groups + 3) / 4 * 4;
   a.splits = plan.splits;
+  a.depth = plan.splits == 1 ? 2 : 1;
   a.stage_wait_ns = stage_wait_limit_ns();
-  const int stage = kWarps * kWeightBlock + plan.splits * 8 * NT * 256;
+  const int stage = a.depth * (kWarps * kWeightBlock + plan.splits * 8 * NT * 256);
   const int fixed = 1024 + kWarps * 8 * kPadded * 4 + 16 * 8 + 16 + 4 * (3 * p.E + 1);
   a.stages = (kLimit - fixed) / stage;
   if (a.stages > 8) a.stages = 8;
@@ -431,6 +452,7 @@ cudaError_t launch_rows(const ProductI4Args& p, const ProductI4Plan& plan, const
 
 cudaError_t launch_product_i4(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
                               const CUtensorMap& map_x, int sms, cudaStream_t stream) {
+  if (plan.tiles) return launch_product_i4_tiles(p, plan.rows, map_w, map_x, sms, stream);
   if (p.gated)
     return p.group == 32   ? launch_rows<32, true>(p, plan, map_w, map_x, sms, stream)
            : p.group == 64 ? launch_rows<64, true>(p, plan, map_w, map_x, sms, stream)
