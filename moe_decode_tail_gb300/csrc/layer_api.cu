@@ -407,15 +407,21 @@ bool encode_i4_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const
   const cuuint32_t box = (cuuint32_t)plan.box_channels, ones[4] = {1, 1, 1, 1};
   const cuuint64_t wd3[3] = {bytes, channels, experts}, wst3[2] = {bytes, bytes * channels};
   const cuuint64_t wd4[4] = {bytes, channels, 2, experts}, wst4[3] = {bytes, bytes * channels, 2 * bytes * channels};
-  const cuuint32_t wb3[3] = {64, box, 1}, wb4[4] = {64, box, 2, 1};
-  const cuuint64_t xd[2] = {(cuuint64_t)D, (cuuint64_t)R}, xst[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t xb[2] = {64, (cuuint32_t)plan.box_rows};
+  const cuuint32_t width = plan.tiles ? 128 : 64;
+  const cuuint32_t wb3[3] = {width, box, 1}, wb4[4] = {width, box, 2, 1};
+  const cuuint64_t row = (cuuint64_t)D * 2;
+  const cuuint64_t xd2[2] = {(cuuint64_t)D, (cuuint64_t)R}, xst2[1] = {row};
+  const cuuint64_t xd3[3] = {64, (cuuint64_t)R, (cuuint64_t)(D / 64)}, xst3[2] = {row, 128};
+  const cuuint32_t xb2[2] = {64, (cuuint32_t)plan.box_rows};
+  const cuuint32_t xb3[3] = {64, (cuuint32_t)plan.box_rows, (cuuint32_t)plan.box_chunks};
+  const bool chunks = plan.box_chunks > 0;
   return enc(map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 4 : 3, const_cast<void*>(w), gated ? wd4 : wd3,
              gated ? wst4 : wst3, gated ? wb4 : wb3, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             plan.tiles ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-         enc(map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), xd, xst, xb, ones,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             plan.tiles ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         enc(map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, chunks ? 3 : 2, const_cast<void*>(x), chunks ? xd3 : xd2,
+             chunks ? xst3 : xst2, chunks ? xb3 : xb2, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int product_i4(const void* x, const void* w, const void* group_scale, const float* channel_scale,

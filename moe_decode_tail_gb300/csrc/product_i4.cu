@@ -390,16 +390,21 @@ ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sm
   ProductI4Plan p;
   const int64_t want = rows_wanted(R, E);
   p.tiles = want > kFewRows;
+  p.wide = false;
   if (p.tiles) {
-    p.rows = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 256 ? 128 : 256;
+    p.rows = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+    const int64_t row_tiles = E == 1 ? (R + 127) / 128 : R / 128 + (R < E ? R : E);
+    p.wide = want > 128 && row_tiles * ((N + 255) / 256) * (gated ? 2 : 1) >= sms;
     p.splits = 0;
-    p.box_channels = gated ? 16 : 128;
+    p.box_channels = (gated ? 64 : 128) * (p.wide ? 2 : 1);
     p.box_rows = p.rows < 64 ? p.rows : 64;
+    p.box_chunks = D % 64 ? 0 : p.rows > 64 ? 1 : 4;
   } else {
     p.rows = want <= 8 ? 8 : want <= 16 ? 16 : 32;
     p.splits = splits_of(R, E, N, (D + 127) / 128, gated, p.rows, blocks_per_sm(p.rows / 8) * sms);
     p.box_channels = (gated ? 16 : kWarpTile) * (kWarps / p.splits);
     p.box_rows = p.rows;
+    p.box_chunks = 0;
   }
   return p;
 }
@@ -452,7 +457,7 @@ cudaError_t launch_rows(const ProductI4Args& p, const ProductI4Plan& plan, const
 
 cudaError_t launch_product_i4(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
                               const CUtensorMap& map_x, int sms, cudaStream_t stream) {
-  if (plan.tiles) return launch_product_i4_tiles(p, plan.rows, map_w, map_x, sms, stream);
+  if (plan.tiles) return launch_product_i4_tiles(p, plan, map_w, map_x, sms, stream);
   if (p.gated)
     return p.group == 32   ? launch_rows<32, true>(p, plan, map_w, map_x, sms, stream)
            : p.group == 64 ? launch_rows<64, true>(p, plan, map_w, map_x, sms, stream)

@@ -1,13 +1,16 @@
 // The 4-bit product on the 5th-generation tensor cores (sm_103a): tiles of 128 channels by 16 to 256 rows.
 //
-// Persistent, one thread block an SM.  The packed weights cross memory once, by TMA (128 channels x 64 bytes, 128 columns of
-// the reduction: a block); sets of four warps turn a block into BF16 in registers, its groups' scales multiplied in, and store
-// it into tensor memory, from where the MMA takes its A operand (a thread's channel is a TMEM lane, so nothing is shuffled
-// or written back to shared memory).  The rows arrive by TMA as the B operand; four warps (eight at 256 rows) read finished
-// accumulators, scale them by channel and write BF16.  The weight stream runs on across tiles.
+// Persistent, one thread block an SM.  The packed weights cross memory once, by TMA (128 channels x 128 bytes, 256 columns of
+// the reduction: a pair of blocks); converting warps, a block of 32 channels each, turn them into BF16 in registers, their
+// groups' scales multiplied in, and store them into tensor memory, from where the MMA takes its A operand (a thread's
+// channel is a TMEM lane, so nothing is shuffled or written back to shared memory).  The rows arrive by TMA as the B operand;
+// four warps (eight at 256 rows) read finished accumulators, scale them by channel and write BF16.  The weight stream runs
+// on across tiles.
 //
-// A gated tile has 64 gate and the 64 up channels that go with them, 16 and 16 in each quarter of the TMEM lanes, so that a
-// pair of lanes 16 apart has both factors of a result.
+// A gated tile has 64 gate channels, then the 64 up channels that go with them; they meet in shared memory.
+//
+// What a step costs the MMA warp besides its MMAs bounds the weight stream with few rows, so that a step is a whole pair then,
+// with one barrier to wait for and one commit (a block a step, two barriers and commits: 570 cycles for 8 KB, 3.3 TB/s).
 //
 // Every wait is bounded in time; on expiry the kernel raises a bit in the device error word, lets its copies and MMAs
 // finish, frees its tensor memory and returns.
@@ -22,19 +25,40 @@ namespace {
 __device__ unsigned int g_i4_tiles_error = 0;
 __device__ __forceinline__ void raise_error(unsigned bit) { atomicOr(&g_i4_tiles_error, bit); }
 
-constexpr int kTileM = 128;               // stored channels of a tile
-constexpr int kWStage = kTileM * 64;      // bytes of a block of them
-constexpr int kAColumns = 64;             // TMEM columns of a block: two BF16 each
-constexpr int kASlots = 4;                // blocks in tensor memory
 constexpr int kRun = 16;                  // accumulator columns (rows of the result) written at a time
-constexpr int kStaging = kRun * kTileM * 2;
+constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
 
-// With few rows the weights' way is the bound and more warps convert; with many the tensor cores.
-constexpr int sets_of(int nt) { return nt > 64 ? 2 : 4; }
-constexpr int readers_of(int nt) { return nt > 128 ? 2 : 1; }  // sets of four epilogue warps (one accumulator: it waits)
-constexpr int threads_of(int nt) { return 32 * (4 * readers_of(nt) + 4 * sets_of(nt) + 3); }
-constexpr int x_columns_of(int nt) { return nt > 128 ? 64 : 128; }  // of the reduction in a stage of rows
-constexpr int x_stages_of(int nt) { return nt > 64 ? 4 : nt == 64 ? 6 : 8; }
+// The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them (two MMAs for the same rows: with
+// many rows it is the rows' way from L2 that bounds, and this halves it).
+template <int NT_, bool WIDE_>
+struct Form {
+  static constexpr int NT = NT_;
+  static constexpr bool WIDE = WIDE_;
+  static constexpr int kSubs = WIDE ? 2 : 1;                        // tiles of 128 stored channels, the MMA's M
+  static constexpr int kWStage = kSubs * 128 * 128;                 // bytes of a pair of blocks of them
+  static constexpr int kBlocks = NT > 64 ? 1 : 2;                   // of a step of the MMA warp
+  static constexpr int kStepsOfPair = 2 / kBlocks;
+  static constexpr int kSlotColumns = 64 * kBlocks * kSubs;         // of a step's A in tensor memory: two BF16 each
+  static constexpr int kAccs = WIDE ? 1 : 2;                        // accumulators, taken in turn
+  static constexpr int kTmemA = kAccs * kSubs * NT;                 // first column of the A ring
+  static constexpr int kSlots = (512 - kTmemA) / kSlotColumns;      // steps in it
+  // Sets of converting warps take the steps in turn, a warp for 32 channels.
+  static constexpr int kSets = WIDE ? 1 : NT > 64 ? 2 : 3;
+  static constexpr int kSetWarps = 4 * kSubs;
+  static constexpr int kReaders = WIDE ? 2 : 1;                     // sets of four epilogue warps (one accumulator: it waits)
+  static constexpr int kEpilogueWarps = 4 * kReaders;
+  static constexpr int kThreads = 32 * (kEpilogueWarps + kSets * kSetWarps + 3);
+  // Rows of a wide tile come in stages of 64 columns, so that a stage is free again soon; the MMA warp waits for those
+  // itself and gives them back.  Others come a step at a time, and their arrival is seen by the converting warps.  Up to 32
+  // rows have twice as many slots as the step ring, so that their copy is asked for well before it is needed; the set that
+  // finds a step's slot free again passes that on.
+  static constexpr bool kJoint = !WIDE, kRelayed = NT <= 32;
+  static constexpr int kXColumns = kJoint ? 128 * kBlocks : 64;
+  static constexpr int kXStages = kRelayed ? 2 * kSlots : kJoint ? kSlots : 6;
+  static constexpr int kXHalf = NT * 128, kXStage = NT * kXColumns * 2;  // bytes of 64 columns, and of a stage
+  static constexpr int kBox = NT < 64 ? NT : 64;                    // rows of one TMA box
+  static_assert(kSlots % kSets == 0, "a set meets the same slots in every round");
+};
 
 struct Args {
   const uint8_t* group_scale;  // e4m3 [E][channels][pitch]
@@ -46,6 +70,7 @@ struct Args {
   int blocks;                  // of 128 columns: ceil(D / 128)
   int groups, pitch;           // scales of a channel, and their distance to the next channel's
   int w_stages;
+  bool whole;                  // D is a multiple of 64: map_x has the columns in sixty-fours
   unsigned long long stage_wait_ns;
 };
 
@@ -55,22 +80,21 @@ struct Tile {
   bool shared;  // more than one row tile reads these weights
 };
 
-// NT: rows of a tile (the accumulator's columns).
-template <int NT, int GROUP, bool GATED>
-__global__ void __launch_bounds__(threads_of(NT), 1)
+template <class F, int GROUP, bool GATED>
+__global__ void __launch_bounds__(F::kThreads, 1)
     product_i4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kReaders = readers_of(NT), kEpilogueWarps = 4 * kReaders, kSets = sets_of(NT), kThreads = threads_of(NT);
-  constexpr int kWarpW = kEpilogueWarps + 4 * kSets, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
-  constexpr int kXColumns = x_columns_of(NT), kXOfBlock = 128 / kXColumns, kXStages = x_stages_of(NT);
-  constexpr int kXHalf = NT * 128, kXStage = NT * kXColumns * 2;  // bytes of 64 columns, and of a stage
-  constexpr int kBox = NT < 64 ? NT : 64;        // rows of one TMA box
-  constexpr int kAccs = NT > 128 ? 1 : 2;        // accumulators, taken in turn
-  constexpr uint32_t kTmemA = kAccs * NT;        // first column of the A ring
+  constexpr int NT = F::NT, kSubs = F::kSubs, kWStage = F::kWStage, kBlocks = F::kBlocks, kStepsOfPair = F::kStepsOfPair;
+  constexpr int kSlotColumns = F::kSlotColumns, kAccs = F::kAccs, kTmemA = F::kTmemA, kSlots = F::kSlots, kSets = F::kSets;
+  constexpr int kSetWarps = F::kSetWarps, kReaders = F::kReaders, kEpilogueWarps = F::kEpilogueWarps;
+  constexpr int kThreads = F::kThreads, kXColumns = F::kXColumns, kXStages = F::kXStages, kXHalf = F::kXHalf;
+  constexpr int kXStage = F::kXStage, kBox = F::kBox;
+  constexpr bool WIDE = F::WIDE, kJoint = F::kJoint, kRelayed = F::kRelayed;
+  constexpr int kWarpW = kEpilogueWarps + kSets * kSetWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
+  constexpr int kXOfStep = 128 * kBlocks / kXColumns;
   constexpr int kPer = 128 / GROUP;              // groups of a block
-  constexpr int kOut = GATED ? 64 : 128;         // channels of the result of a tile
-  static_assert(kTmemA + kASlots * kAColumns <= 512, "tensor memory");
-  static_assert(kASlots % kSets == 0, "a set meets the same slots in every round");
+  constexpr int kHalf = 64 * kSubs;              // of a gated tile: gate channels, then up channels
+  constexpr int kOut = GATED ? kHalf : 2 * kHalf;  // channels of the result of a tile
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_addr(smem_raw);
@@ -78,15 +102,16 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   uint8_t* base_ptr = smem_raw + (base - raw);
   const uint32_t x_ring = base, w_ring = x_ring + (uint32_t)(kXStages * kXStage);
   uint32_t at = w_ring + (uint32_t)(a.w_stages * kWStage);
-  const uint32_t staging = at + (warp >> 2) % kReaders * kStaging;  // an epilogue set's BF16
+  const uint32_t staging = at + (warp >> 2) % kReaders * kStaging;  // of an epilogue set
   at += kReaders * kStaging;
   auto bars = [&](int n) {
     const uint32_t first = at;
     at += 8u * n;
     return first;
   };
-  const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages), x_full = bars(kXStages), x_empty = bars(kXStages);
-  const uint32_t a_full = bars(kASlots), a_empty = bars(kASlots);
+  const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages), x_full = bars(kXStages);
+  const uint32_t step_full = bars(kSlots), step_empty = bars(kSlots);
+  const uint32_t x_empty = kJoint && !kRelayed ? step_empty : bars(kXStages);
   const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
   at = (at + 15u) & ~15u;
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort
@@ -99,15 +124,15 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
   if (warp == 0) {
     for (int s = lane; s < a.w_stages; s += 32) {
       mbar_init(w_full + 8 * s, 1);
-      mbar_init(w_empty + 8 * s, 4);  // a set of four warps reads it
+      mbar_init(w_empty + 8 * s, kBlocks == 2 ? kSetWarps : kSets * kSetWarps);  // one set reads it, or all of them
     }
     for (int s = lane; s < kXStages; s += 32) {
       mbar_init(x_full + 8 * s, 1);
-      mbar_init(x_empty + 8 * s, 1);
+      if (!kJoint || kRelayed) mbar_init(x_empty + 8 * s, 1);
     }
-    if (lane < kASlots) {
-      mbar_init(a_full + 8 * lane, 4);
-      mbar_init(a_empty + 8 * lane, 1);
+    if (lane < kSlots) {
+      mbar_init(step_full + 8 * lane, kSetWarps);
+      mbar_init(step_empty + 8 * lane, 1);
     }
     if (lane < kAccs) {
       mbar_init(acc_full + 8 * lane, 1);
@@ -155,6 +180,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     q.shared = row_tiles > 1;
     return true;
   };
+  const int pairs = (a.blocks + 1) / 2;  // an odd last block has one of zeros beside it
   auto give_up = [&](unsigned bit) {
     if (!*abort_ptr) raise_error(bit);
     *abort_ptr = 1;
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
       const uint64_t policy = q.shared ? again : once;
-      for (int b = 0; b < a.blocks; ++b, ++g, w.step(a.w_stages)) {
+      for (int b = 0; b < pairs; ++b, ++g, w.step(a.w_stages)) {
         if (!warp_wait(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
@@ -180,12 +206,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         if (elect_one()) {
           const uint32_t dst = w_ring + w.slot * kWStage, bar = w_full + 8 * w.slot;
           mbar_expect_tx(bar, kWStage);
-          if (GATED) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) tma_load_4d(dst + p * (kWStage / 4), &map_w, bar, 64 * b, q.n0 + 16 * p, 0, q.e, policy);
-          } else {
-            tma_load_3d(dst, &map_w, bar, 64 * b, q.n0, q.e, policy);
-          }
+          if (GATED) tma_load_4d(dst, &map_w, bar, 128 * b, q.n0, 0, q.e, policy);
+          else tma_load_3d(dst, &map_w, bar, 128 * b, q.n0, q.e, policy);
         }
         __syncwarp();
       }
@@ -203,19 +225,26 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
       const int boxes = NT <= kBox ? 1 : (q.rows + kBox - 1) / kBox;
-      for (int b = 0; b < kXOfBlock * a.blocks; ++b, ++g, x.step(kXStages)) {
+      for (int b = 0; b < kXOfStep * kStepsOfPair * pairs; ++b, ++g, x.step(kXStages)) {
         if (!warp_wait(x_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
           break;
         }
         if (elect_one()) {
-          mbar_expect_tx(x_full + 8 * x.slot, (uint32_t)(kXColumns / 64 * boxes * kBox * 128));
+          const uint32_t dst = x_ring + x.slot * kXStage, bar = x_full + 8 * x.slot;
+          mbar_expect_tx(bar, (uint32_t)(kXColumns / 64 * boxes * kBox * 128));
+          if (a.whole && kBox == NT) {
+            tma_load_3d(dst, &map_x, bar, 0, q.r0, kXColumns / 64 * b, keep);
+          } else {
 #pragma unroll
-          for (int h = 0; h < kXColumns / 64; ++h)
-            for (int c = 0; c < boxes; ++c)
-              tma_load_2d(x_ring + x.slot * kXStage + h * kXHalf + c * kBox * 128, &map_x, x_full + 8 * x.slot,
-                          kXColumns * b + 64 * h, q.r0 + c * kBox, keep);
+            for (int h = 0; h < kXColumns / 64; ++h)
+              for (int c = 0; c < boxes; ++c) {
+                const uint32_t to = dst + h * kXHalf + c * kBox * 128;
+                if (a.whole) tma_load_3d(to, &map_x, bar, 0, q.r0 + c * kBox, kXColumns / 64 * b + h, keep);
+                else tma_load_2d(to, &map_x, bar, kXColumns * b + 64 * h, q.r0 + c * kBox, keep);
+              }
+          }
         }
         __syncwarp();
       }
@@ -235,32 +264,41 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         if (lane == 0) give_up(kErrWaitAccum);
         break;
       }
-      const uint32_t idesc = idesc_bf16(kTileM, (q.rows + 15) & ~15);
-      const uint32_t d = tmem + acc.slot * NT;
-      for (int b = 0; ok && b < a.blocks; ++b, s.step(kASlots)) {
-        ok = warp_wait(a_full + 8 * s.slot, s.parity, abort_ptr, limit);
-        const uint32_t w = tmem + kTmemA + s.slot * kAColumns;
+      const uint32_t idesc = idesc_bf16(128, (q.rows + 15) & ~15);
+      const uint32_t d = tmem + acc.slot * (kSubs * NT);
+      const int steps = kStepsOfPair * pairs;
+      for (int b = 0; b < steps; ++b, s.step(kSlots)) {
+        if (!warp_wait(step_full + 8 * s.slot, s.parity, abort_ptr, limit)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
+          break;
+        }
+        const uint32_t w = tmem + kTmemA + s.slot * kSlotColumns;
 #pragma unroll
-        for (int h = 0; h < kXOfBlock; ++h) {
-          ok = ok && warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr, limit);
-          if (!ok) break;
+        for (int h = 0; h < kXOfStep; ++h, x.step(kXStages)) {
+          if (!kJoint && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr, limit)) {
+            if (lane == 0) give_up(kErrWaitFull);
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint64_t bdesc = smem_desc_sw128(x_ring + x.slot * kXStage);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kXColumns / 16; ++kk)  // 16 columns: 8 TMEM columns of A, 32 bytes along B's swizzled row
-              mma_ts(d, w + 32 * h + 8 * kk, bdesc + (kk / 4) * (kXHalf >> 4) + 2 * (kk % 4), idesc,
-                     (b > 0 || h > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(x_empty + 8 * x.slot);
-            if (h == kXOfBlock - 1) {
-              mma_commit(a_empty + 8 * s.slot);
-              if (b == a.blocks - 1) mma_commit(acc_full + 8 * acc.slot);
+#pragma unroll
+              for (int m = 0; m < kSubs; ++m)
+                mma_ts(d + m * NT, w + 64 * kBlocks * m + 32 * h + 8 * kk, bdesc + (kk / 4) * (kXHalf >> 4) + 2 * (kk % 4), idesc,
+                       (b > 0 || h > 0 || kk > 0) ? 1u : 0u);
+            if (!kJoint) mma_commit(x_empty + 8 * x.slot);
+            if (h == kXOfStep - 1) {
+              mma_commit(step_empty + 8 * s.slot);
+              if (b == steps - 1) mma_commit(acc_full + 8 * acc.slot);
             }
           }
           __syncwarp();
-          x.step(kXStages);
         }
-        if (!ok && lane == 0) give_up(kErrWaitFull);
+        if (!kJoint && !ok) break;
       }
     }
     if (elect_one()) mma_commit(mma_done);  // the MMAs that were issued are done before tensor memory is freed
@@ -269,93 +307,131 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
     __syncwarp();
   } else if (warp >= kEpilogueWarps) {
     // ---------------- 4 bits to BF16, one TMEM lane a thread ----------------
-    // Set s takes the blocks s, s + kSets, ... of the stream.
-    const int set = (warp - kEpilogueWarps) >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane, swizzle = (row >> 1) & 3;  // 16-byte units of a 64-byte row, as the copy lays them
+    // Set s takes the steps s, s + kSets, ... of the stream: pairs, or one block of each (two sets), or both in turn (one).
+    const int set = (warp - kEpilogueWarps) / kSetWarps, sub = (warp - kEpilogueWarps) % kSetWarps >> 2, quarter = warp & 3;
+    const int row = sub * 128 + quarter * 32 + lane;   // of the staged tile
     const int channels = GATED ? 2 * a.N : a.N;
-    Ring w;
-    w.step(a.w_stages, set);
-    uint32_t parity = 0;  // of the set's rounds through its slots in tensor memory
-    int slot_a = set;
-    int ahead = set;      // blocks until this set's next one
-    bool ok = true;
+    constexpr int kStride = kBlocks == 2 ? kSets : 1;  // pairs from one of a set to its next
+    constexpr int kMine = kBlocks == 2 ? 1 : 2 / kSets;  // steps of a pair
+    constexpr int kGroups = kPer * kBlocks * kMine, kWords = (kGroups + 3) / 4;  // of these: their scales, in words of four
+    const int first_block = kBlocks == 1 && kSets == 2 ? set : 0;                // of a pair
+    Ring w, s, x;
+    int ahead = kBlocks == 2 ? set : 0;                // pairs until this set's next one
+    w.step(a.w_stages, ahead);
+    s.step(kSlots, set);
+    x.step(kXStages, set);
+    bool ok = true, second_round = false;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
       // this thread's channel; past the last: the last
-      const int past = GATED && (lane & 16) ? a.N : 0;
-      const int n = min(q.n0 + (GATED ? 16 * quarter + (lane & 15) : row), a.N - 1) + past;
+      const int n = min(q.n0 + (GATED ? row % kHalf : row), a.N - 1) + (GATED && row >= kHalf ? a.N : 0);
       const uint8_t* scales = a.group_scale + ((int64_t)q.e * channels + n) * a.pitch;
-      auto four_scales = [&](int block) {  // of them those of a block
-        return block < a.blocks ? __ldg(reinterpret_cast<const uint32_t*>(scales + (block * kPer & ~3))) : 0u;
+      auto load_scales = [&](int pair, uint32_t (&to)[kWords]) {  // the words with those of its steps
+        const int first = (2 * pair + first_block) * kPer & ~3;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          to[k] = first + 4 * k < a.groups ? __ldg(reinterpret_cast<const uint32_t*>(scales + first + 4 * k)) : 0u;
       };
-      uint32_t next = four_scales(ahead);
-      for (; ahead < a.blocks; ahead += kSets, w.step(a.w_stages, kSets)) {
-        uint32_t gs = next;
-        next = four_scales(ahead + kSets);
-        const int left = a.groups - (ahead * kPer & ~3);  // behind the last group may stand anything: it counts as zero
-        if (left < 4) gs &= (1u << (8 * left)) - 1u;
-        gs >>= 8 * (ahead * kPer & 3);
+      uint32_t next[kWords];
+      load_scales(ahead, next);
+      for (; ahead < pairs; ahead += kStride, w.step(a.w_stages, kStride)) {
+        const int first = (2 * ahead + first_block) * kPer;  // group
+        uint32_t gs[kWords];
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          gs[k] = next[k];
+          const int left = a.groups - (first & ~3) - 4 * k;  // behind the last group may stand anything: it counts as zero
+          if (left < 4) gs[k] &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
+        }
+        if (kGroups < 4) gs[0] >>= 8 * (first & 3);
+        load_scales(ahead + kStride, next);
         if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
           break;
         }
-        const uint32_t src = w_ring + w.slot * kWStage + row * 64;
-        uint4 v[4];  // words 4 t + i: columns 32 i + 8 t ..
-#pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = ld_shared_v4(src + ((t ^ swizzle) << 4));
-        const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + slot_a * kAColumns;
         Factors f;
+        uint4 v[4];  // words 4 t + i: columns 32 i + 8 t .. of a block
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 64 columns
-          uint32_t r[32];
+        for (int step = 0; step < kMine; ++step, s.step(kSlots, kSets), x.step(kXStages, kSets)) {
+          const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + s.slot * kSlotColumns + sub * 64 * kBlocks;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = 2 * h + j;
-            if (32 * c % GROUP == 0) f = scaled(gs >> (8 * (32 * c / GROUP)));
+          for (int h = 0; h < 2 * kBlocks; ++h) {  // 64 columns
+            if (h % 2 == 0) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              int4x8_to_bf16(c == 0 ? v[t].x : c == 1 ? v[t].y : c == 2 ? v[t].z : v[t].w, f, r + 16 * j + 4 * t);
+              for (int t = 0; t < 4; ++t)
+                v[t] = ld_shared_v4(w_ring + w.slot * kWStage + sw128_offset(row, 4 * (first_block + step + h / 2) + t));
+            }
+            uint32_t r[32];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = 4 * step + 2 * h + j, group = 32 * c / GROUP;
+              if (32 * c % GROUP == 0) f = scaled(gs[group / 4] >> (8 * (group % 4)));
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                int4x8_to_bf16(c % 4 == 0 ? v[t].x : c % 4 == 1 ? v[t].y : c % 4 == 2 ? v[t].z : v[t].w, f, r + 16 * j + 4 * t);
+            }
+            if (h == 0) {
+              ok = warp_wait(step_empty + 8 * s.slot, s.parity ^ 1u, abort_ptr);
+              if (!ok) break;
+              tc_fence_after();
+              // the step that had this slot before is done, and so are its rows
+              if (kRelayed && second_round && quarter == 0 && lane == 0)
+                mbar_arrive(x_empty + 8 * (x.slot < kSlots ? x.slot + kSlots : x.slot - kSlots));
+              second_round = true;
+            }
+            tmem_st32(dst + 32 * h, r);
           }
-          if (h == 0) {
-            ok = warp_wait(a_empty + 8 * slot_a, parity ^ 1u, abort_ptr);
-            if (!ok) break;
-            tc_fence_after();
+          if (!ok) {
+            if (lane == 0) give_up(kErrWaitEmpty);
+            break;
           }
-          tmem_st32(dst + 32 * h, r);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
+          if (step == kMine - 1 && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
+          // one warp of the set sees the rows arrive too, so that the MMA warp has one barrier to wait for
+          if (kJoint && quarter == 0 && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr)) {
+            if (lane == 0) give_up(kErrWaitFull);
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(step_full + 8 * s.slot);
         }
-        if (!ok) {
-          if (lane == 0) give_up(kErrWaitEmpty);
-          break;
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
-        if (lane == 0) {
-          mbar_arrive(w_empty + 8 * w.slot);
-          mbar_arrive(a_full + 8 * slot_a);
-        }
-        slot_a += kSets;
-        if (slot_a >= kASlots) {
-          slot_a -= kASlots;
-          parity ^= 1u;
-        }
+        if (!ok) break;
       }
-      ahead -= a.blocks;
+      ahead -= pairs;
     }
   } else {
     // ---------------- accumulators to BF16 ----------------
-    // A set of four warps reads every kReaders-th run of 16 columns.
-    const int reader = warp >> 2, quarter = warp & 3;
+    // A wide tile's result stays in registers until the accumulators have been read and given back.  Its two sets of four
+    // warps read one of the two accumulators each, or, gated, every second run of 16 columns of both.
+    const int reader = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const int channels = GATED ? 2 * a.N : a.N;
-    const int mine = GATED ? 16 * quarter + (lane & 15) : 32 * quarter + lane;  // of the tile's channels of the result
+    // this thread's channel of the result, and from which accumulator, of the tile's first
+    const int mine = WIDE ? row + (GATED ? 0 : 128 * reader) : GATED ? row & 63 : row;
+    auto value = [](uint32_t bits) { return __uint_as_float(bits); };
+    // 16 rows of 128 channels (of a narrow gated tile, 64) of this set, as they lie in shared memory, to the result
+    auto store = [&](const Tile& q, int c, int n0, auto eight) {
+      constexpr int kVectors = GATED && !WIDE ? 8 : 16;  // of a row
+#pragma unroll
+      for (int k = row; k < kRun * kVectors; k += 128) {
+        const int r = k / kVectors, u = k % kVectors;
+        const uint4 out = eight(r, u);
+        if (c + r < q.rows && n0 + 8 * u < a.N) st_v4(a.out + (int64_t)(q.r0 + c + r) * a.N + n0 + 8 * u, out);
+      }
+    };
+    auto bf16_rows = [&](int r, int u) { return ld_shared_v4(staging + (r * 128 + 8 * u) * 2); };
     Ring acc;
     bool ok = true;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x, acc.step(kAccs)) {
-      const int past = GATED && (lane & 16) ? a.N : 0;
-      const float cs = q.n0 + mine < a.N ? kScaled * __ldg(a.channel_scale + (int64_t)q.e * channels + q.n0 + mine + past) : 0.0f;
+      const float* cs_at = a.channel_scale + (int64_t)q.e * channels + q.n0 + mine;
+      const bool there = q.n0 + mine < a.N;
+      const float cs = there ? kScaled * __ldg(cs_at + (GATED && !WIDE && row >= 64 ? a.N : 0)) : 0.0f;
+      const float cs_up = GATED && WIDE && there ? kScaled * __ldg(cs_at + a.N) : 0.0f;
       ok = warp_wait(acc_full + 8 * acc.slot, acc.parity, abort_ptr);
       ok = all_of<32 * kEpilogueWarps>(ok);  // one answer for the warps that meet at barriers below
       if (!ok) {
@@ -363,44 +439,89 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
         break;
       }
       tc_fence_after();
-      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + acc.slot * NT;
-#pragma unroll 1
-      for (int c = kRun * reader; c < q.rows; c += kRun * kReaders) {
-        float v[kRun];
-        together();
-        tmem_ld16(src + c, v);
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + acc.slot * (kSubs * NT);
+      if constexpr (WIDE) {
+        constexpr int kRuns = NT / kRun / (GATED ? 2 : 1);  // of a set
+        uint32_t two[kRuns][kRun / 2];                      // two rows of this thread's channel
+        auto first_row = [&](int k) { return kRun * (GATED ? 2 * k + reader : k); };
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) v[j] *= cs;
-        // By shared memory, so that a row's channels leave as whole lines.
-        if (GATED) {
-          // the lower lanes take the first eight rows, the upper ones the others: each sends the factors the other lacks
+        for (int k = 0; k < kRuns; ++k) {
+          const int c = first_row(k);
+          if (c >= q.rows) continue;
+          float v[kRun];
+          together();
+          tmem_ld16(src + (GATED ? 0 : reader * NT) + c, v);
+          if (GATED) {
+            float u[kRun];
+            together();
+            tmem_ld16(src + NT + c, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_xor_sync(0xffffffffu, lane & 16 ? v[j] : v[8 + j], 16);
-            const float y = silu_times(lane & 16 ? other : v[j], lane & 16 ? v[8 + j] : other);
-            st_shared_u16(staging + ((j + (lane & 16 ? 8 : 0)) * 64 + mine) * 2, bf16x2_pz(y, y));
+            for (int j = 0; j < kRun; ++j) v[j] = silu_times(v[j] * cs, u[j] * cs_up);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) v[j] *= cs;
           }
-        } else {
+#pragma unroll
+          for (int j = 0; j < kRun; j += 2) two[k][j / 2] = bf16x2_pz(v[j], v[j + 1]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * acc.slot);
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+          const int c = first_row(k);
+          if (c >= q.rows) continue;
 #pragma unroll
           for (int j = 0; j < kRun; j += 2) {
-            const uint32_t two = bf16x2_pz(v[j], v[j + 1]);
-            st_shared_u16(staging + (j * kTileM + mine) * 2, two);
-            st_shared_u16(staging + ((j + 1) * kTileM + mine) * 2, two >> 16);
+            st_shared_u16(staging + (j * 128 + row) * 2, two[k][j / 2]);
+            st_shared_u16(staging + ((j + 1) * 128 + row) * 2, two[k][j / 2] >> 16);
           }
+          set_bar(reader);
+          store(q, c, q.n0 + (GATED ? 0 : 128 * reader), bf16_rows);
+          set_bar(reader);
         }
-        set_bar(reader);
-        constexpr int kVectors = kOut / 8;  // of a row
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < q.rows; c += kRun) {
+          float v[kRun];
+          together();
+          tmem_ld16(src + c, v);
 #pragma unroll
-        for (int k = quarter * 32 + lane; k < kRun * kVectors; k += 128) {
-          const int r = k / kVectors, u = k % kVectors;
-          const uint4 eight = ld_shared_v4(staging + 16 * k);
-          if (c + r < q.rows && q.n0 + 8 * u < a.N) st_v4(a.out + (int64_t)(q.r0 + c + r) * a.N + q.n0 + 8 * u, eight);
+          for (int j = 0; j < kRun; ++j) v[j] *= cs;
+          // By shared memory, so that a row's channels leave as whole lines, and a gate meets its up.
+          if (GATED) {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) st_shared_f32(staging + (j * 128 + row) * 4, v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kRun; j += 2) {
+              const uint32_t two = bf16x2_pz(v[j], v[j + 1]);
+              st_shared_u16(staging + (j * 128 + row) * 2, two);
+              st_shared_u16(staging + ((j + 1) * 128 + row) * 2, two >> 16);
+            }
+          }
+          set_bar(reader);
+          if (GATED) {
+            store(q, c, q.n0, [&](int r, int u) {
+              uint32_t y[4];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint4 g = ld_shared_v4(staging + (r * 128 + 8 * u + 4 * j) * 4);
+                const uint4 up = ld_shared_v4(staging + (r * 128 + 64 + 8 * u + 4 * j) * 4);
+                y[2 * j] = bf16x2_pz(silu_times(value(g.x), value(up.x)), silu_times(value(g.y), value(up.y)));
+                y[2 * j + 1] = bf16x2_pz(silu_times(value(g.z), value(up.z)), silu_times(value(g.w), value(up.w)));
+              }
+              return make_uint4(y[0], y[1], y[2], y[3]);
+            });
+          } else {
+            store(q, c, q.n0, bf16_rows);
+          }
+          set_bar(reader);
         }
-        set_bar(reader);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * acc.slot);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + 8 * acc.slot);
     }
   }
   tc_fence_before();
@@ -411,9 +532,9 @@ __global__ void __launch_bounds__(threads_of(NT), 1)
 
 // ---- host --------------------------------------------------------------------------------------------------------------
 
-template <int NT, int GROUP, bool GATED>
-cudaError_t launch_nt(const ProductI4Args& p, const CUtensorMap& map_w, const CUtensorMap& map_x, int sms, cudaStream_t stream) {
-  constexpr int kLimit = 227 * 1024, kXRing = x_stages_of(NT) * NT * x_columns_of(NT) * 2, kOut = GATED ? 64 : 128;
+template <class F, int GROUP, bool GATED>
+cudaError_t launch_form(const ProductI4Args& p, const CUtensorMap& map_w, const CUtensorMap& map_x, int sms, cudaStream_t stream) {
+  constexpr int kLimit = 227 * 1024, kXRing = F::kXStages * F::kXStage, kOut = (GATED ? 64 : 128) * F::kSubs;
   Args a;
   a.group_scale = p.group_scale;
   a.channel_scale = p.channel_scale;
@@ -426,45 +547,47 @@ cudaError_t launch_nt(const ProductI4Args& p, const CUtensorMap& map_w, const CU
   a.groups = (p.D + GROUP - 1) / GROUP;
   a.pitch = (a.groups + 3) / 4 * 4;
   a.stage_wait_ns = stage_wait_limit_ns();
-  const int fixed = 1024 + readers_of(NT) * kStaging + 8 * (2 * 16 + 2 * 8 + 2 * kASlots + 2 * 2 + 1) + 32 + 4 * (3 * p.E + 1);
-  a.w_stages = (kLimit - fixed - kXRing) / kWStage;
-  if (a.w_stages > 16) a.w_stages = 16;
-  // A set of converting warps must meet the same slots in every round: else it could ask for a slot's next round while
-  // another set's copy in it is still on its way, and the parity of the round before would tell it that its own had landed.
-  a.w_stages -= a.w_stages % sets_of(NT);
-  auto kernel = product_i4_tiles_kernel<NT, GROUP, GATED>;
+  const int fixed = 1024 + F::kReaders * kStaging + 8 * (2 * 12 + 2 * 6 + 2 * 4 + 2 * 2 + 1) + 32 + 4 * (3 * p.E + 1);
+  a.w_stages = (kLimit - fixed - kXRing) / F::kWStage;
+  if (a.w_stages > 12) a.w_stages = 12;
+  // A set of converting warps that takes every third pair must meet the same slots in every round: else it could ask for
+  // a slot's next round while another set's copy in it is still on its way, and the parity of the round before would tell
+  // it that its own had landed.
+  if (F::kBlocks == 2) a.w_stages -= a.w_stages % F::kSets;
+  a.whole = p.D % 64 == 0;
+  auto kernel = product_i4_tiles_kernel<F, GROUP, GATED>;
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
   if (e != cudaSuccess) return e;
   // no more thread blocks than there can be tiles
-  const int64_t row_tiles = p.E == 1 ? (p.R + NT - 1) / NT : p.R / NT + (p.R < p.E ? p.R : p.E);
+  const int64_t row_tiles = p.E == 1 ? (p.R + F::NT - 1) / F::NT : p.R / F::NT + (p.R < p.E ? p.R : p.E);
   const int64_t most = row_tiles * ((p.N + kOut - 1) / kOut);
-  return launch_pdl(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(threads_of(NT)),
-                    (size_t)fixed + kXRing + (size_t)a.w_stages * kWStage, stream, map_w, map_x, a);
+  return launch_pdl(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(F::kThreads),
+                    (size_t)fixed + kXRing + (size_t)a.w_stages * F::kWStage, stream, map_w, map_x, a);
 }
 
 template <int GROUP, bool GATED>
-cudaError_t launch_rows(const ProductI4Args& p, int rows, const CUtensorMap& map_w, const CUtensorMap& map_x, int sms,
-                        cudaStream_t stream) {
-  switch (rows) {
-    case 16: return launch_nt<16, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    case 32: return launch_nt<32, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    case 64: return launch_nt<64, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    case 128: return launch_nt<128, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    default: return launch_nt<256, GROUP, GATED>(p, map_w, map_x, sms, stream);
+cudaError_t launch_rows(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w, const CUtensorMap& map_x,
+                        int sms, cudaStream_t stream) {
+  if (plan.wide) return launch_form<Form<128, true>, GROUP, GATED>(p, map_w, map_x, sms, stream);
+  switch (plan.rows) {
+    case 16: return launch_form<Form<16, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
+    case 32: return launch_form<Form<32, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
+    case 64: return launch_form<Form<64, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
+    default: return launch_form<Form<128, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_product_i4_tiles(const ProductI4Args& p, int rows, const CUtensorMap& map_w, const CUtensorMap& map_x,
-                                    int sms, cudaStream_t stream) {
+cudaError_t launch_product_i4_tiles(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
+                                    const CUtensorMap& map_x, int sms, cudaStream_t stream) {
   if (p.gated)
-    return p.group == 32   ? launch_rows<32, true>(p, rows, map_w, map_x, sms, stream)
-           : p.group == 64 ? launch_rows<64, true>(p, rows, map_w, map_x, sms, stream)
-                           : launch_rows<128, true>(p, rows, map_w, map_x, sms, stream);
-  return p.group == 32   ? launch_rows<32, false>(p, rows, map_w, map_x, sms, stream)
-         : p.group == 64 ? launch_rows<64, false>(p, rows, map_w, map_x, sms, stream)
-                         : launch_rows<128, false>(p, rows, map_w, map_x, sms, stream);
+    return p.group == 32   ? launch_rows<32, true>(p, plan, map_w, map_x, sms, stream)
+           : p.group == 64 ? launch_rows<64, true>(p, plan, map_w, map_x, sms, stream)
+                           : launch_rows<128, true>(p, plan, map_w, map_x, sms, stream);
+  return p.group == 32   ? launch_rows<32, false>(p, plan, map_w, map_x, sms, stream)
+         : p.group == 64 ? launch_rows<64, false>(p, plan, map_w, map_x, sms, stream)
+                         : launch_rows<128, false>(p, plan, map_w, map_x, sms, stream);
 }
 
 cudaError_t take_product_i4_tiles_error(unsigned* bits) {

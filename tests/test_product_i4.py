@@ -165,6 +165,23 @@ def test_weights_that_stream(R, E, D, N, gated):
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("R,E,D,N,group", [(3000, 8, 1024, 1288, 128), (5000, 2, 392, 2056, 64), (2600, 1, 2056, 2568, 32),
+                                           (9000, 60, 264, 1416, 32), (4100, 3, 640, 1800, 64)])
+def test_many_rows(R, E, D, N, group, gated):
+    # enough tiles for the wide ones, experts with one row tile and with many
+    g = gen(R)
+    weight = Weight(g, E, 2 * N if gated else N, D, group)
+    ids = (torch.rand((R, E), generator=g, device="cuda") * torch.linspace(1.0, 4.0, E, device="cuda")).argmax(1)
+    offsets = offsets_of(torch.bincount(ids, minlength=E).cpu()) if E > 1 else None
+    x = normal(g, R, D)
+    out = call(x, weight, offsets, gated)
+    again = [call(x, weight, offsets, gated) for _ in range(4)]
+    check(out, x, weight, offsets, gated)
+    assert all(torch.equal(o, out) for o in again)
+    assert mt.moe_tail_take_device_error() == 0
+
+
+@pytest.mark.parametrize("gated", [False, True])
 def test_values_that_are_not_finite_stay_in_their_rows_and_channels(gated):
     g = gen(2)
     N, D = 96, 520
