@@ -169,15 +169,16 @@ struct ProductI4Args {
 struct ProductI4Plan {
   bool tiles, wide;  // tiles on the tensor cores (product_i4_tiles.cu); else warps that multiply (product_i4.cu)
   int rows;          // of a tile
-  int splits;        // warps along the reduction (no tiles)
+  int box_columns;   // bytes of a channel in a box of w
   int box_channels;  // of one half of a gated weight, or of a plain one, in a box of w
   int box_rows;      // in a box of x
   int box_chunks;    // of 64 columns in a box of x, or 0: x is read as two dimensions
 };
 ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sms);
-// map_w: w as [E][channels][64 ceil(D / 128)] bytes, gated as [E][2][N][...], in boxes of (2 x) box_channels x 128 bytes with
-// the 128-byte swizzle (tiles), or x 64 bytes without one.  map_x: x as [R][D] in boxes of box_rows x 64, or as
-// [D / 64][R][64] in boxes of box_chunks x box_rows x 64, with the 128-byte swizzle.  Zeros out of range.
+// map_w: w as [E][channels][64 ceil(D / 128)] bytes, gated as [E][2][N][...], in boxes of (2 x) box_channels x box_columns
+// bytes; with tiles in bytes with the 128-byte swizzle, else in words of four bytes without one.  map_x: x as [R][D] in boxes
+// of box_rows x 64, or as [D / 64][R][64] in boxes of box_chunks x box_rows x 64, with the 128-byte swizzle.  Zeros out of
+// range.
 cudaError_t launch_product_i4(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,
                               const CUtensorMap& map_x, int sms, cudaStream_t stream);
 cudaError_t launch_product_i4_tiles(const ProductI4Args& p, const ProductI4Plan& plan, const CUtensorMap& map_w,

@@ -403,11 +403,12 @@ bool encode_i4_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const
                     bool gated, const moetail::ProductI4Plan& plan) {
   EncodeTiled enc = encoder();
   if (!enc) return false;
-  const cuuint64_t bytes = 64 * (cuuint64_t)((D + 127) / 128), channels = (cuuint64_t)N, experts = (cuuint64_t)E;
+  const cuuint64_t bytes = 64 * (cuuint64_t)((D + 127) / 128), element = plan.tiles ? 1 : 4, columns = bytes / element;
+  const cuuint64_t channels = (cuuint64_t)N, experts = (cuuint64_t)E;
   const cuuint32_t box = (cuuint32_t)plan.box_channels, ones[4] = {1, 1, 1, 1};
-  const cuuint64_t wd3[3] = {bytes, channels, experts}, wst3[2] = {bytes, bytes * channels};
-  const cuuint64_t wd4[4] = {bytes, channels, 2, experts}, wst4[3] = {bytes, bytes * channels, 2 * bytes * channels};
-  const cuuint32_t width = plan.tiles ? 128 : 64;
+  const cuuint64_t wd3[3] = {columns, channels, experts}, wst3[2] = {bytes, bytes * channels};
+  const cuuint64_t wd4[4] = {columns, channels, 2, experts}, wst4[3] = {bytes, bytes * channels, 2 * bytes * channels};
+  const cuuint32_t width = (cuuint32_t)(plan.box_columns / element);
   const cuuint32_t wb3[3] = {width, box, 1}, wb4[4] = {width, box, 2, 1};
   const cuuint64_t row = (cuuint64_t)D * 2;
   const cuuint64_t xd2[2] = {(cuuint64_t)D, (cuuint64_t)R}, xst2[1] = {row};
@@ -415,7 +416,8 @@ bool encode_i4_maps(CUtensorMap* map_w, CUtensorMap* map_x, const void* w, const
   const cuuint32_t xb2[2] = {64, (cuuint32_t)plan.box_rows};
   const cuuint32_t xb3[3] = {64, (cuuint32_t)plan.box_rows, (cuuint32_t)plan.box_chunks};
   const bool chunks = plan.box_chunks > 0;
-  return enc(map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, gated ? 4 : 3, const_cast<void*>(w), gated ? wd4 : wd3,
+  return enc(map_w, plan.tiles ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT32, gated ? 4 : 3,
+             const_cast<void*>(w), gated ? wd4 : wd3,
              gated ? wst4 : wst3, gated ? wb4 : wb3, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
              plan.tiles ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
