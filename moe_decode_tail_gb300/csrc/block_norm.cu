@@ -22,9 +22,14 @@
 // blocks, whose warps write their sums into one another's shared memory.
 #include <float.h>
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "kernels.h"
 #include "layer.h"
 #include "rows.cuh"
+#include "tensor_core.cuh"
 
 namespace moetail {
 
@@ -132,10 +137,14 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) block_norm_kernel(const
 
 // ---- gradient ------------------------------------------------------------------------------------------------------
 
+__device__ unsigned int g_norm_error = 0;
+
 constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
-constexpr int kGradColumns = 8 * kGradThreads;  // columns of a thread block
-constexpr int kMaxCluster = 8;                  // thread blocks of a row: 32768 columns
+constexpr int kGroupColumns = 2048;  // of a row that shares its thread block with others
+constexpr int kMaxCluster = 8;       // thread blocks of a row: 32768 columns, eight a thread
 constexpr int kMaxGradBlocks = 160;
+constexpr int kLeastWarps = 4;       // one for each tensor of a row in shared memory
+constexpr int kStagedBytes = 200 * 1024;  // of rows in shared memory
 
 // How a call's rows lie on thread blocks.
 struct GradShape {
@@ -144,189 +153,388 @@ struct GradShape {
   int warps;      // of a row in a thread block
   int groups;     // rows at a time of a thread block
   int row_sets;   // clusters: sets of rows with their own column sums
+  int stages;     // of rows in shared memory, 0: rows go to registers
 };
-GradShape grad_shape(int b, int H, int blocks) {
+int least_cluster(int H) { return (H + 8 * kGradThreads - 1) / (8 * kGradThreads); }
+GradShape grad_shape(int H, int cluster) {
   GradShape s;
-  const int nv = H >> 3;
-  s.cluster = 1;
-  while (s.cluster * kGradThreads < nv) s.cluster *= 2;
-  s.vectors = (nv + s.cluster - 1) / s.cluster;
+  s.cluster = cluster;
+  s.vectors = ((H >> 3) + cluster - 1) / cluster;
   s.warps = (s.vectors + 31) / 32;
-  s.groups = s.cluster > 1 ? 1 : kGradWarps / s.warps;
-  const int most = blocks / s.cluster, needed = (b + s.groups - 1) / s.groups;
-  s.row_sets = needed < most ? needed : most;
+  const bool staged = H > kGroupColumns;
+  s.groups = staged ? 1 : kGradWarps / s.warps;
+  s.stages = staged ? kStagedBytes / (64 * s.vectors) : 0;
+  if (s.stages > 8) s.stages = 8;
+  s.row_sets = 0;
   return s;
 }
-
-// The sum over a row's threads, the same in all of them: a warp's by shuffles, then the warps' in a fixed order.  The warps'
-// sums meet in slots 0 and 1 in turn: a thread that has passed the barrier of one knows that the other has been read.
-template <bool CLUSTER>
-__device__ __forceinline__ float row_sum(float v, int& turn, int group, int warps, int warp, float (*s_sum)[kMaxCluster * kGradWarps]) {
-  const int lane = threadIdx.x & 31, slot = turn;
-  turn ^= 1;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if (CLUSTER) {
-    const int ranks = (int)cluster_size();
-    if (lane < ranks) st_cluster_f32(map_to_rank(smem_addr(&s_sum[slot][cluster_rank() * kGradWarps + warp]), lane), v);
-    cluster_sync_all();
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxCluster * kGradWarps; i += 32) {
-      const int w = i + lane;
-      if (w < ranks * kGradWarps && w % kGradWarps < warps) v += s_sum[slot][w];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  } else if (warps > 1) {
-    if (lane == 0) s_sum[slot][group * warps + warp] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
-    v = lane < warps ? s_sum[slot][group * warps + lane] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  }
-  return v;
+int row_sets(int b, int groups, int most) {
+  const int needed = (b + groups - 1) / groups;
+  return needed < most ? needed : most;
 }
 
-template <bool POST, bool CHANNEL, bool CLUSTER>
-__global__ void __launch_bounds__(kGradThreads, 1) block_norm_grad_kernel(const BlockNormGradArgs a, const GradShape s) {
-  __shared__ float s_sum[2][kMaxCluster * kGradWarps];
-  __shared__ float s_columns[kGradWarps][256];  // a warp's columns
-  const int group = (threadIdx.x >> 5) / s.warps, warp = (threadIdx.x >> 5) - group * s.warps;
-  const int t = threadIdx.x - 32 * group * s.warps;  // the thread's vector in its thread block's part of the row
-  const int part = CLUSTER ? (int)cluster_rank() : 0;
-  const int64_t set = CLUSTER ? blockIdx.x / cluster_size() : blockIdx.x;
-  const int v = part * s.vectors + t;
-  const bool live = t < s.vectors && 8 * v < a.H;
-  if (CLUSTER) cluster_sync_all();  // its thread blocks have started, so that their shared memory can be written
-  grid_dependency_wait();
-  launch_dependents();
-
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 post = zero, pre = zero, channel = zero;
-  if (live) {
+// The columns' factors, as they are stored.
+template <bool POST, bool CHANNEL>
+struct Columns {
+  uint4 post, pre, channel;
+  __device__ __forceinline__ void load(const BlockNormGradArgs& a, int v, bool live) {
+    post = pre = channel = make_uint4(0, 0, 0, 0);
+    if (!live) return;
     pre = ld_v4(a.pre_gamma + 8 * v);
     if (POST) post = ld_v4(a.post_gamma + 8 * v);
     if (CHANNEL) channel = ld_v4(a.channel_gate + 8 * v);
   }
-  float sum_pre[8], sum_post[8], sum_channel[8];
+};
+template <bool POST, bool CHANNEL>
+struct Sums {
+  float2 pre[4], post[4], channel[4];
+  __device__ __forceinline__ Sums() {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum_pre[e] = sum_post[e] = sum_channel[e] = 0.0f;
-
-  struct Row {
-    uint4 x, residual, d_y, d_residual;
-    float rstd0, rstd1, token;
-  };
-  const int64_t stride = (int64_t)s.row_sets * s.groups;
-  auto load = [&](int64_t row, Row& r) {
-    r = Row{zero, zero, zero, zero, 0.0f, 0.0f, 1.0f};
-    if (row >= a.b) return;
-    if (live) {
-      const int64_t at = row * a.H + 8 * v;
-      r.x = ld_rows(a.x + at);
-      r.residual = ld_rows(a.residual + at);
-      r.d_y = ld_rows(a.d_y + at);
-      if (a.d_residual_out) r.d_residual = ld_rows(a.d_residual_out + at);
-    }
-    r.rstd0 = a.rstd[2 * row];
-    r.rstd1 = a.rstd[2 * row + 1];
-    if (a.token_gate) r.token = a.token_gate[row];
-  };
-  Row next;
-  int64_t row = set * s.groups + group;
-  int turn = 0;
-  load(row, next);
-  for (; row < a.b; row += stride) {
-    const Row r = next;
-    load(row + stride, next);
-    float x[8], n[8], c[8], h[8], d[8], g[8];
-    unpack8(r.x, x);
-    unpack8(r.residual, h);
-    unpack8(r.d_y, d);
-    unpack8(pre, g);
-    if (CHANNEL) unpack8(channel, c);
-    if (POST) {
-      float p[8];
-      unpack8(post, p);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] *= r.rstd0;  // u
-        n[e] = x[e] * (p[e] + a.gain_center);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = x[e];
-    }
-    float dot = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float gate = CHANNEL ? r.token * c[e] : r.token;
-      h[e] = (a.residual_scale * h[e] + gate * n[e]) * r.rstd1;  // v
-      sum_pre[e] += d[e] * h[e];
-      d[e] *= g[e] + a.gain_center;  // d_v
-      dot += d[e] * h[e];
-    }
-    const float mean = row_sum<CLUSTER>(dot, turn, group, s.warps, warp, s_sum) * a.rcpH;
-    const int64_t at = row * a.H + 8 * v;
-    unpack8(r.d_residual, g);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = g[e] + r.rstd1 * (d[e] - h[e] * mean);  // d_h
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = a.residual_scale * d[e];
-    if (live) st_v4(a.d_residual + at, pack8_pz(h));
-    dot = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float dn = d[e] * n[e];
-      if (CHANNEL) sum_channel[e] += r.token * dn;
-      dot += CHANNEL ? c[e] * dn : dn;
-    }
-    float d_token = 0.0f;
-    if (POST || a.d_token_gate) d_token = row_sum<CLUSTER>(dot, turn, group, s.warps, warp, s_sum);
-    if (a.d_token_gate && t == 0 && part == 0) a.d_token_gate[row] = d_token;
-    const float mean_u = r.token * d_token * a.rcpH;
-    if (POST) {
-      float p[8];
-      unpack8(post, p);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] *= CHANNEL ? r.token * c[e] : r.token;  // d_n
-        sum_post[e] += d[e] * x[e];
-        d[e] = r.rstd0 * (d[e] * (p[e] + a.gain_center) - x[e] * mean_u);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] *= CHANNEL ? r.token * c[e] : r.token;
-    }
-    if (live) st_v4(a.d_x + at, pack8_pz(d));
+    for (int e = 0; e < 4; ++e) pre[e] = post[e] = channel[e] = make_float2(0.0f, 0.0f);
   }
+};
+struct Row {
+  float rstd0, rstd1, token;
+  __device__ __forceinline__ void load(const BlockNormGradArgs& a, int64_t row) {
+    rstd0 = rstd1 = 0.0f;
+    token = 1.0f;
+    if (row >= a.b) return;
+    rstd0 = a.rstd[2 * row];
+    rstd1 = a.rstd[2 * row + 1];
+    if (a.token_gate) token = a.token_gate[row];
+  }
+};
 
-  // The column sums of the thread block's groups, in their order, to this set's rows of the workspace.
-  float* out = a.partial + set * 3 * a.H;
-  auto leave = [&](float (&sum)[8], float* to) {
-    __syncthreads();
-    if (group > 0) {
+// Eight columns of a row, two at a time.
+template <bool POST, bool CHANNEL>
+struct Values {
+  float2 u[4], n[4], v[4], d_v[4];
+  // From x, residual and d_y; returns the columns' part of the sum of d_v * v.
+  __device__ __forceinline__ float form(const BlockNormGradArgs& a, const Row& r, const Columns<POST, CHANNEL>& c, uint4 x,
+                                        uint4 residual, uint4 d_y) {
+    float2 g[4], h[4], dot = make_float2(0.0f, 0.0f);
+    unpack8p(x, u);
+    if (POST) {
+      unpack8p(c.post, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_columns[threadIdx.x >> 5][32 * e + (threadIdx.x & 31)] = sum[e];
-    }
-    __syncthreads();
-    if (group == 0 && live) {
-      for (int i = 1; i < s.groups; ++i)
+      for (int e = 0; e < 4; ++e) {
+        u[e] = mul2(u[e], splat2(r.rstd0));
+        n[e] = mul2(u[e], add2(g[e], splat2(a.gain_center)));
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += s_columns[i * s.warps + warp][32 * e + (threadIdx.x & 31)];
-      *reinterpret_cast<float4*>(to + 8 * v) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      *reinterpret_cast<float4*>(to + 8 * v + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      for (int e = 0; e < 4; ++e) n[e] = u[e];
     }
-  };
-  if (POST && a.d_post_gamma) leave(sum_post, out);
-  if (a.d_pre_gamma) leave(sum_pre, out + a.H);
-  if (CHANNEL && a.d_channel_gate) leave(sum_channel, out + 2 * a.H);
+    unpack8p(residual, h);
+    if (CHANNEL) unpack8p(c.channel, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 gate = CHANNEL ? mul2(g[e], splat2(r.token)) : splat2(r.token);
+      v[e] = mul2(fma2(gate, n[e], mul2(h[e], splat2(a.residual_scale))), splat2(r.rstd1));
+    }
+    unpack8p(d_y, d_v);
+    unpack8p(c.pre, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d_v[e] = mul2(d_v[e], add2(g[e], splat2(a.gain_center)));
+      dot = fma2(d_v[e], v[e], dot);
+    }
+    return dot.x + dot.y;
+  }
+  // d_h in the place of d_v, given the mean of d_v * v; returns the columns' part of the sum of d_h * channel_gate * n.
+  __device__ __forceinline__ float inner(const BlockNormGradArgs& a, const Row& r, const Columns<POST, CHANNEL>& c,
+                                         Sums<POST, CHANNEL>& sums, float mean, uint4 d_y, uint4 d_residual) {
+    float2 g[4], dot = make_float2(0.0f, 0.0f);
+    unpack8p(d_y, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sums.pre[e] = fma2(g[e], v[e], sums.pre[e]);
+      d_v[e] = fma2(v[e], splat2(-mean), d_v[e]);
+    }
+    unpack8p(d_residual, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d_v[e] = fma2(d_v[e], splat2(r.rstd1), g[e]);
+    if (CHANNEL) unpack8p(c.channel, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 d_n = mul2(d_v[e], n[e]);
+      if (CHANNEL) {
+        sums.channel[e] = fma2(d_n, splat2(r.token), sums.channel[e]);
+        dot = fma2(d_n, g[e], dot);
+      } else {
+        dot = add2(dot, d_n);
+      }
+    }
+    return dot.x + dot.y;
+  }
+};
+__device__ __forceinline__ uint4 packed(const float2 (&v)[4]) {
+  return make_uint4(bf16x2_pz(v[0].x, v[0].y), bf16x2_pz(v[1].x, v[1].y), bf16x2_pz(v[2].x, v[2].y), bf16x2_pz(v[3].x, v[3].y));
+}
+__device__ __forceinline__ uint4 packed(const float2 (&v)[4], float scale) {
+  float2 w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = mul2(v[e], splat2(scale));
+  return packed(w);
+}
+// d_x of eight columns from their d_h and u, given the mean of d_u * u.
+template <bool POST, bool CHANNEL>
+__device__ __forceinline__ uint4 outer(const BlockNormGradArgs& a, const Row& r, const Columns<POST, CHANNEL>& c,
+                                       Sums<POST, CHANNEL>& sums, const float2 (&d_h)[4], const float2 (&u)[4], float mean) {
+  float2 g[4], d[4];
+  if (CHANNEL) unpack8p(c.channel, g);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] = mul2(d_h[e], CHANNEL ? mul2(g[e], splat2(r.token)) : splat2(r.token));  // d_n
+  if (POST) {
+    unpack8p(c.post, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sums.post[e] = fma2(d[e], u[e], sums.post[e]);
+      d[e] = mul2(fma2(d[e], add2(g[e], splat2(a.gain_center)), mul2(u[e], splat2(-mean))), splat2(r.rstd0));
+    }
+  }
+  return packed(d);
 }
 
-// The sets' column sums added in their order: a warp takes every eighth set for 128 columns.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, int sets, int H, float* d_post, float* d_pre,
-                                                          float* d_channel) {
-  __shared__ float4 s_part[8][32];
+__device__ __forceinline__ void st_columns(float* to, const float2 (&sum)[4]) {
+  *reinterpret_cast<float4*>(to) = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
+  *reinterpret_cast<float4*>(to + 4) = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
+}
+
+// Rows of at most 2048 columns: a group of warps each, the next row's loads in flight.
+template <bool POST, bool CHANNEL>
+__global__ void __launch_bounds__(kGradThreads, 1) grad_groups_kernel(const BlockNormGradArgs a, const GradShape s) {
+  __shared__ float s_sum[2][kGradWarps];
+  __shared__ float2 s_columns[kGradWarps][4 * 32];  // a warp's columns
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / s.warps, warp = (threadIdx.x >> 5) - group * s.warps;
+  const int v = 32 * warp + lane;  // this thread's vector of a row
+  const bool live = v < s.vectors;
+  grid_dependency_wait();
+  launch_dependents();
+  // The sum over a row's threads, the same in all of them, the warps' in a fixed order.  They meet in slots 0 and 1 in turn:
+  // a thread that has passed the barrier of one knows that the other has been read.
+  int slot = 0;
+  auto row_sum = [&](float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if (s.warps > 1) {
+      if (lane == 0) s_sum[slot][group * s.warps + warp] = x;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * s.warps) : "memory");
+      x = lane < s.warps ? s_sum[slot][group * s.warps + lane] : 0.0f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      slot ^= 1;
+    }
+    return x;
+  };
+  Columns<POST, CHANNEL> columns;
+  columns.load(a, v, live);
+  Sums<POST, CHANNEL> sums;
+  struct Loads {
+    uint4 x, residual, d_y, d_residual;
+    Row row;
+  } next;
+  auto load = [&](int64_t row) {
+    next.x = next.residual = next.d_y = next.d_residual = make_uint4(0, 0, 0, 0);
+    next.row.load(a, row);
+    if (row >= a.b || !live) return;
+    const int64_t at = row * a.H + 8 * v;
+    next.x = ld_rows(a.x + at);
+    next.residual = ld_rows(a.residual + at);
+    next.d_y = ld_rows(a.d_y + at);
+    if (a.d_residual_out) next.d_residual = ld_rows(a.d_residual_out + at);
+  };
+  const int64_t stride = (int64_t)s.row_sets * s.groups;
+  int64_t row = (int64_t)blockIdx.x * s.groups + group;
+  load(row);
+  for (; row < a.b; row += stride) {
+    const Loads l = next;
+    load(row + stride);
+    Values<POST, CHANNEL> w;
+    const float mean = row_sum(w.form(a, l.row, columns, l.x, l.residual, l.d_y)) * a.rcpH;
+    float dot = w.inner(a, l.row, columns, sums, mean, l.d_y, l.d_residual);
+    const int64_t at = row * a.H + 8 * v;
+    if (live) st_v4(a.d_residual + at, packed(w.d_v, a.residual_scale));
+    if (POST || a.d_token_gate) dot = row_sum(dot);
+    if (a.d_token_gate && v == 0) a.d_token_gate[row] = dot;
+    const uint4 d_x = outer(a, l.row, columns, sums, w.d_v, w.u, l.row.token * dot * a.rcpH);
+    if (live) st_v4(a.d_x + at, d_x);
+  }
+  // The groups' column sums in their order, to this thread block's rows of the workspace.
+  float* out = a.partial + (int64_t)blockIdx.x * 3 * a.H;
+  auto leave = [&](float2 (&sum)[4], float* to) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_columns[threadIdx.x >> 5][32 * e + lane] = sum[e];
+    __syncthreads();
+    if (group > 0 || !live) return;
+    for (int i = 1; i < s.groups; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], s_columns[i * s.warps + warp][32 * e + lane]);
+    st_columns(to + 8 * v, sum);
+  };
+  if (POST && a.d_post_gamma) leave(sums.post, out);
+  if (a.d_pre_gamma) leave(sums.pre, out + a.H);
+  if (CHANNEL && a.d_channel_gate) leave(sums.channel, out + 2 * a.H);
+}
+
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32x2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
+// Wider rows: a row's (or a cluster's part of a row's) x, residual, d_y and d_residual_out arrive in shared memory, several
+// rows ahead, and each row has one barrier: the second sum of a row and the first of the next meet at it.
+template <bool POST, bool CHANNEL, bool CLUSTER>
+__global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const BlockNormGradArgs a, const GradShape s) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ float2 s_sum[2][kMaxCluster * kGradWarps];
+  __shared__ __align__(8) uint64_t s_bar[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = CLUSTER ? (int)cluster_rank() : 0, ranks = CLUSTER ? (int)cluster_size() : 1;
+  const int64_t set = CLUSTER ? blockIdx.x / ranks : blockIdx.x;
+  const int first = part * s.vectors, vectors = min(s.vectors, (a.H >> 3) - first);
+  const uint32_t row_bytes = 16u * vectors, stage_bytes = 64u * s.vectors, base = smem_addr(smem_raw), bars = smem_addr(s_bar);
+  const int tensors = a.d_residual_out ? 4 : 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < s.stages; ++i) mbar_init(bars + 8 * i, tensors);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (CLUSTER) cluster_sync_all();  // its thread blocks have started, so that their shared memory can be written
+  else __syncthreads();
+  grid_dependency_wait();
+  launch_dependents();
+
+  const int64_t stride = (int64_t)s.row_sets * a.H;            // elements from one row of this set to its next
+  const int rows = (int)((a.b - set + s.row_sets - 1) / s.row_sets);  // at least one
+  // One lane of each of the first warps brings a tensor's part of a row (one thread for all of them kept its warp, and so
+  // every barrier, waiting).
+  const uint16_t* source = nullptr;
+  if (lane == 0 && warp < tensors)
+    source = (warp == 0 ? a.x : warp == 1 ? a.residual : warp == 2 ? a.d_y : a.d_residual_out) + set * a.H + 8 * first;
+  const uint32_t apart = 16u * s.vectors;
+  int brought = 0;
+  auto bring = [&](uint32_t stage) {
+    if (source == nullptr || brought >= rows) return;
+    mbar_expect_tx(bars + 8 * stage, row_bytes);
+    copy_bulk(base + stage * stage_bytes + warp * apart, source, row_bytes, bars + 8 * stage);
+    source += stride;
+    ++brought;
+  };
+  for (int i = 0; i < s.stages; ++i) bring(i);
+
+  // This thread's vector of the thread block's part.  Threads past the last read what is there and add nothing to the sums.
+  const int v = threadIdx.x;
+  const bool live = v < vectors;
+  Columns<POST, CHANNEL> columns;
+  columns.load(a, first + v, live);
+  Sums<POST, CHANNEL> sums;
+  auto wait = [&](uint32_t stage, uint32_t parity) {
+    if (!mbar_wait(bars + 8 * stage, parity)) atomicOr(&g_norm_error, kErrWaitFull);
+  };
+  // Two sums over the row, the same in every thread, in a fixed order; slots in turn as for the groups.
+  int slot = 0;
+  auto row_sums = [&](float x, float y) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, off);
+      y += __shfl_xor_sync(0xffffffffu, y, off);
+    }
+    if (CLUSTER) {
+      if (lane < ranks) st_cluster_f32x2(map_to_rank(smem_addr(&s_sum[slot][part * kGradWarps + warp]), lane), x, y);
+      cluster_sync_all();
+    } else {
+      if (lane == 0) s_sum[slot][warp] = make_float2(x, y);
+      __syncthreads();
+    }
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < (CLUSTER ? kMaxCluster : 1) * kGradWarps; i += 32) {
+      const int w = i + lane;
+      if (w < ranks * kGradWarps && w % kGradWarps < s.warps) sum = add2(sum, s_sum[slot][w]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, off);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, off);
+    }
+    slot ^= 1;
+    return sum;
+  };
+  Values<POST, CHANNEL> w;  // of the row at hand
+  // The rows' scalars: a lane loads those of one row in 32 (loads in flight across the waits below made every row wait for them).
+  Row of_lane;
+  auto row_at = [&](int k) {  // called for 0, 1, 2, ..
+    if (k % 32 == 0) of_lane.load(a, k + lane < rows ? set + (int64_t)(k + lane) * s.row_sets : a.b);
+    Row row;
+    row.rstd0 = __shfl_sync(0xffffffffu, of_lane.rstd0, k % 32);
+    row.rstd1 = __shfl_sync(0xffffffffu, of_lane.rstd1, k % 32);
+    row.token = __shfl_sync(0xffffffffu, of_lane.token, k % 32);
+    return row;
+  };
+  Row r = row_at(0);
+  const uint32_t mine = base + 16u * v;
+  auto form = [&](const Row& row, uint32_t at) {
+    const float dot = w.form(a, row, columns, ld_shared_v4(at), ld_shared_v4(at + apart), ld_shared_v4(at + 2 * apart));
+    return live ? dot : 0.0f;
+  };
+  wait(0, 0);
+  float mean = row_sums(0.0f, form(r, mine)).y * a.rcpH;
+  uint32_t stage = 0, parity = 0, at = mine;
+  uint16_t *d_x = a.d_x + set * a.H + 8 * (first + v), *d_residual = a.d_residual + set * a.H + 8 * (first + v);
+  float* d_token = a.d_token_gate && threadIdx.x == 0 && part == 0 ? a.d_token_gate + set : nullptr;
+  for (int k = 0; k < rows; ++k) {
+    const uint4 d_out = a.d_residual_out ? ld_shared_v4(at + 3 * apart) : make_uint4(0, 0, 0, 0);
+    float dot = w.inner(a, r, columns, sums, mean, ld_shared_v4(at + 2 * apart), d_out);
+    if (!live) dot = 0.0f;
+    if (live) st_v4(d_residual, packed(w.d_v, a.residual_scale));
+    d_residual += stride;
+    float2 d_h[4], u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d_h[e] = w.d_v[e];
+      u[e] = w.u[e];
+    }
+    const Row here = r;
+    const uint32_t read = stage;
+    at += stage_bytes;
+    if (++stage == (uint32_t)s.stages) {
+      stage = 0;
+      at = mine;
+      parity ^= 1u;
+    }
+    float dot_next = 0.0f;
+    if (k + 1 < rows) {
+      r = row_at(k + 1);
+      wait(stage, parity);
+      dot_next = form(r, at);
+    }
+    const float2 both = row_sums(dot, dot_next);
+    bring(read);  // past the barrier every thread has read this row
+    if (d_token) {
+      *d_token = both.x;
+      d_token += s.row_sets;
+    }
+    const uint4 out = outer(a, here, columns, sums, d_h, u, here.token * both.x * a.rcpH);
+    if (live) st_v4(d_x, out);
+    d_x += stride;
+    mean = both.y * a.rcpH;
+  }
+  float* out = a.partial + set * 3 * a.H + 8 * (first + v);
+  if (!live) return;
+  if (POST && a.d_post_gamma) st_columns(out, sums.post);
+  if (a.d_pre_gamma) st_columns(out + a.H, sums.pre);
+  if (CHANNEL && a.d_channel_gate) st_columns(out + 2 * a.H, sums.channel);
+}
+
+// The sets' column sums added in their order: a warp takes every 32nd set for 128 columns, their loads in flight together.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partial, int sets, int H, float* d_post, float* d_pre,
+                                                           float* d_channel) {
+  __shared__ float4 s_part[32][32];
   grid_dependency_wait();
   launch_dependents();
   float* out = blockIdx.y == 0 ? d_post : blockIdx.y == 1 ? d_pre : d_channel;
@@ -335,8 +543,8 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, 
   const int c = blockIdx.x * 128 + 4 * lane;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < H) {
-#pragma unroll 4
-    for (int i = warp; i < sets; i += 8) {
+#pragma unroll 5
+    for (int i = warp; i < sets; i += 32) {
       const float4 p = __ldcg(reinterpret_cast<const float4*>(partial + ((int64_t)i * 3 + blockIdx.y) * H + c));
       sum.x += p.x;
       sum.y += p.y;
@@ -346,16 +554,12 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* partial, 
   }
   s_part[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && c < H) {
+  const int column = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && column < H) {
+    float total = 0.0f;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) {
-      const float4 p = s_part[w][lane];
-      sum.x += p.x;
-      sum.y += p.y;
-      sum.z += p.z;
-      sum.w += p.w;
-    }
-    *reinterpret_cast<float4*>(out + c) = sum;
+    for (int w = 0; w < 32; ++w) total += reinterpret_cast<const float*>(s_part[w])[threadIdx.x];
+    out[column] = total;
   }
 }
 
@@ -379,36 +583,98 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, int sms, cudaStream_t stre
 }
 
 size_t block_norm_grad_workspace(int b, int H) {
-  return (size_t)grad_shape(b, H, kMaxGradBlocks).row_sets * 3 * H * sizeof(float);
+  const GradShape s = grad_shape(H, least_cluster(H));
+  return (size_t)row_sets(b, s.groups, kMaxGradBlocks / s.cluster) * 3 * H * sizeof(float);
 }
 
-cudaError_t launch_block_norm_grad(const BlockNormGradArgs& a, int sms, cudaStream_t stream) {
-  const GradShape s = grad_shape(a.b, a.H, sms < kMaxGradBlocks ? sms : kMaxGradBlocks);
+namespace {
+
+// The clusters of a launch that fit the current device at once, asked once for each kernel, shape and device: clusters lie
+// within a part of the GPU, so that there are fewer of some sizes than the SMs divided by their size.
+int clusters_at_once(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster) {
+  static std::mutex m;
+  static std::map<std::tuple<const void*, int, unsigned, size_t, int>, int> known;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  std::lock_guard<std::mutex> lock(m);
+  int& found = known[{kernel, dev, cfg.blockDim.x, cfg.dynamicSmemBytes, cluster}];
+  if (found == 0) {
+    cudaLaunchConfig_t only = cfg;  // without the other attribute
+    only.attrs = cfg.attrs + 1;
+    only.numAttrs = 1;
+    found = cudaOccupancyMaxActiveClusters(&n, kernel, &only) == cudaSuccess && n > 0 ? n : 1;
+    (void)cudaGetLastError();
+  }
+  return found;
+}
+
+template <bool POST, bool CHANNEL>
+cudaError_t launch_grad(const BlockNormGradArgs& a, int most, int* sets, cudaStream_t stream) {
+  GradShape s = grad_shape(a.H, least_cluster(a.H));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s.row_sets * s.cluster);
-  cfg.blockDim = dim3(32 * s.warps * s.groups);  // every thread takes part in a row: the cluster's barriers count them all
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)s.cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = s.cluster > 1 ? 2 : 1;
+  cfg.stream = stream;
+  auto shape = [&](int cluster) {
+    s = grad_shape(a.H, cluster);
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(32 * s.warps * s.groups);  // every thread takes part in a row: its barriers count them all
+    cfg.dynamicSmemBytes = s.stages ? (size_t)s.stages * 64 * s.vectors + 512 : 0;  // threads past the last vector read on
+  };
+  shape(s.cluster);
+  auto kernel = s.stages == 0 ? grad_groups_kernel<POST, CHANNEL>
+                : s.cluster > 1 ? grad_staged_kernel<POST, CHANNEL, true>
+                                : grad_staged_kernel<POST, CHANNEL, false>;
+  if (s.stages > 0) {
+    const cudaError_t e = ensure_smem_limit((const void*)kernel, kStagedBytes + 512);
+    if (e != cudaSuccess) return e;
+  }
+  int at_once = most / s.cluster;
+  if (s.cluster > 1) {  // the size of which the most SMs have a thread block
+    int best = s.cluster, best_blocks = 0;
+    for (int c = s.cluster; c <= kMaxCluster && a.H >= 8 * 32 * kLeastWarps * c; ++c) {
+      shape(c);
+      const int n = clusters_at_once((const void*)kernel, cfg, c);
+      if (n * c > best_blocks) {
+        best = c;
+        best_blocks = n * c;
+        at_once = n < most / c ? n : most / c;
+      }
+    }
+    shape(best);
+  }
+  s.row_sets = *sets = row_sets(a.b, s.groups, at_once);
+  cfg.gridDim = dim3(s.row_sets * s.cluster);
+  return cudaLaunchKernelEx(&cfg, kernel, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm_grad(const BlockNormGradArgs& a, int sms, cudaStream_t stream) {
+  const int most = sms < kMaxGradBlocks ? sms : kMaxGradBlocks;
+  int sets = 0;  // no rows: no sets, and the sums are zeros
   cudaError_t e = cudaSuccess;
   if (a.b > 0) {
-    auto launch = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, s); };
-#define MOE_PICK(POST, CHANNEL) \
-  (s.cluster > 1 ? launch(block_norm_grad_kernel<POST, CHANNEL, true>) : launch(block_norm_grad_kernel<POST, CHANNEL, false>))
-    e = a.post_gamma ? (a.channel_gate ? MOE_PICK(true, true) : MOE_PICK(true, false))
-                     : (a.channel_gate ? MOE_PICK(false, true) : MOE_PICK(false, false));
-#undef MOE_PICK
+    e = a.post_gamma ? (a.channel_gate ? launch_grad<true, true>(a, most, &sets, stream) : launch_grad<true, false>(a, most, &sets, stream))
+                     : (a.channel_gate ? launch_grad<false, true>(a, most, &sets, stream) : launch_grad<false, false>(a, most, &sets, stream));
     if (e != cudaSuccess) return e;
   }
   if (!a.d_post_gamma && !a.d_pre_gamma && !a.d_channel_gate) return e;
-  // no rows: no sets, and the sums are zeros
-  return launch_pdl(column_sums_kernel, dim3((a.H + 127) / 128, 3), dim3(256), 0, stream, (const float*)a.partial, s.row_sets,
+  return launch_pdl(column_sums_kernel, dim3((a.H + 127) / 128, 3), dim3(1024), 0, stream, (const float*)a.partial, sets,
                     a.H, a.d_post_gamma, a.d_pre_gamma, a.d_channel_gate);
+}
+
+cudaError_t take_block_norm_error(unsigned* bits) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_error, sizeof v);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_norm_error, &zero, sizeof zero);
+  *bits = v;
+  return e;
 }
 
 }  // namespace moetail

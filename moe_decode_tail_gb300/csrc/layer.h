@@ -91,6 +91,7 @@ struct BlockNormGradArgs {
 };
 cudaError_t launch_block_norm_grad(const BlockNormGradArgs& a, int sms, cudaStream_t stream);
 size_t block_norm_grad_workspace(int b, int H);
+cudaError_t take_block_norm_error(unsigned* bits);
 
 // ---- routes (routes.cu) ----------------------------------------------------------
 

@@ -616,13 +616,14 @@ MOE_API const char* moe_tail_status_str(int status) {
 
 MOE_API int moe_tail_take_device_error(unsigned int* bits) {
   if (!bits) return MOE_TAIL_EINVAL;
-  unsigned g = 0, f = 0, p = 0, q = 0, t = 0;
+  unsigned g = 0, f = 0, p = 0, q = 0, t = 0, n = 0;
   cudaError_t e = moetail::take_device_error(&g);
   if (e == cudaSuccess) e = moetail::take_finalize_error(&f);
   if (e == cudaSuccess) e = moetail::take_product_error(&p);
   if (e == cudaSuccess) e = moetail::take_product_i4_error(&q);
   if (e == cudaSuccess) e = moetail::take_product_i4_tiles_error(&t);
-  *bits = g | f | p | q | t;
+  if (e == cudaSuccess) e = moetail::take_block_norm_error(&n);
+  *bits = g | f | p | q | t | n;
   return finish(e);
 }
 

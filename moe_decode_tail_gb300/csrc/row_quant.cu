@@ -188,12 +188,6 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_quant_kernel(const
   store_rows<KIND, GROUPED, VPT>(h, largest, row, nv, a.q, a.scale, a.groups);
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-  return pair_of(d);
-}
-
 // silu(g) * up = g * up / (1 + exp(-g)) for two columns, within 10 units in the last place.  With e = exp(-|g| / 2): for
 // g >= 0 the divisor is 1 + e^2; for g < 0 the fraction is multiplied by e^2 above and below, one e with each factor, so
 // that nothing leaves FP32's range before the result does.

@@ -59,6 +59,12 @@ __device__ __forceinline__ RowSums block_reduce(float sum, uint32_t top) {
   return RowSums{sum, top};
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(d);
+}
+
 // Eight values in BF16, -0 made +0.
 __device__ __forceinline__ uint4 pack8_pz(const float (&v)[8]) {
   return make_uint4(bf16x2_pz(v[0], v[1]), bf16x2_pz(v[2], v[3]), bf16x2_pz(v[4], v[5]), bf16x2_pz(v[6], v[7]));
