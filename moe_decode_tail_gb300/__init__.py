@@ -144,13 +144,25 @@ def _cuda(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
-def _cuda_here(*ts):
-    """Contiguous CUDA tensors of the current device, which is where a call launches its kernels."""
-    _cuda(*ts)
-    here = torch.cuda.current_device()
-    for t in ts:
+def _operands(*operands) -> None:
+    """Operands (name, tensor or None, dtype, shape): each of that type and shape, contiguous and on the current device, which
+    is where a call launches its kernels.  One look at each where all is well, since the host's time counts in decode."""
+    try:
+        here = torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):  # a torch without this function, which is not public, or without a GPU
+        here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for _, t, dtype, shape in operands:
+        if t is not None and not (t.get_device() == here and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+            break
+    else:
+        return
+    for name, t, dtype, shape in operands:
+        if t is not None:
+            _like(name, t, dtype, shape)
+    for name, t, _, _ in operands:
+        _cuda(t)
         if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors must be on the current device, cuda:{here}, got {t.device}")
+            raise ValueError(f"{name} must be on the current device, cuda:{here}, got {t.device}")
 
 
 def _dims(name: str, t, n: int) -> tuple:
@@ -495,16 +507,6 @@ def moe_tail_silu_quant(gate_up, q, scale, *, used_rows=None, group=0, stream=No
     return q, scale
 
 
-def _rows_and_vectors(shape, rows, vectors) -> None:
-    """Named BF16 rows of one shape [b, H], and vectors [H] of a type; those that are None are left out."""
-    for name, t in rows.items():
-        if t is not None:
-            _like(name, t, torch.bfloat16, shape)
-    for name, (t, dtype, length) in vectors.items():
-        if t is not None:
-            _like(name, t, dtype, (length,))
-
-
 def moe_tail_block_norm(x, residual, post_gamma, pre_gamma, residual_out, y, *, token_gate=None, channel_gate=None, rstd=None,
                         residual_scale=1.0, gain_center=1.0, eps=1e-6, stream=None):
     """h = residual_scale * residual + token_gate * channel_gate * n into residual_out, n the RMS norm of x with gains
@@ -514,12 +516,9 @@ def moe_tail_block_norm(x, residual, post_gamma, pre_gamma, residual_out, y, *, 
     moe_tail_block_norm_grad.  Returns (residual_out, y)."""
     shape = b, H = _dims("x", x, 2)
     bf, f32 = torch.bfloat16, torch.float32
-    _rows_and_vectors(shape, {"x": x, "residual": residual, "residual_out": residual_out, "y": y},
-                      {"post_gamma": (post_gamma, bf, H), "pre_gamma": (pre_gamma, bf, H), "token_gate": (token_gate, f32, b),
-                       "channel_gate": (channel_gate, bf, H)})
-    if rstd is not None:
-        _like("rstd", rstd, f32, (b, 2))
-    _cuda_here(x, residual, post_gamma, pre_gamma, residual_out, y, token_gate, channel_gate, rstd)
+    _operands(("x", x, bf, shape), ("residual", residual, bf, shape), ("post_gamma", post_gamma, bf, (H,)),
+              ("pre_gamma", pre_gamma, bf, (H,)), ("residual_out", residual_out, bf, shape), ("y", y, bf, shape),
+              ("token_gate", token_gate, f32, (b,)), ("channel_gate", channel_gate, bf, (H,)), ("rstd", rstd, f32, (b, 2)))
     _check("moe_tail_block_norm", lib().moe_tail_block_norm(
         _p(x), _p(residual), _p(post_gamma), _p(pre_gamma), _p(token_gate), _p(channel_gate), residual_scale, gain_center, eps,
         b, H, _p(residual_out), _p(y), _p(rstd), _stream(stream)))
@@ -543,15 +542,13 @@ def moe_tail_block_norm_grad(d_y, d_residual_out, x, residual, post_gamma, pre_g
                            ("d_channel_gate", d_channel_gate, channel_gate)):
         if grad is not None and of is None:
             raise ValueError(f"{name} must be None where {name[2:]} is")
-    _rows_and_vectors(shape, {"d_y": d_y, "d_residual_out": d_residual_out, "x": x, "residual": residual, "d_x": d_x,
-                              "d_residual": d_residual},
-                      {"post_gamma": (post_gamma, bf, H), "pre_gamma": (pre_gamma, bf, H), "token_gate": (token_gate, f32, b),
-                       "channel_gate": (channel_gate, bf, H), "d_post_gamma": (d_post_gamma, f32, H),
-                       "d_pre_gamma": (d_pre_gamma, f32, H), "d_token_gate": (d_token_gate, f32, b),
-                       "d_channel_gate": (d_channel_gate, f32, H)})
-    _like("rstd", rstd, f32, (b, 2))
-    _cuda_here(d_y, d_residual_out, x, residual, post_gamma, pre_gamma, rstd, d_x, d_residual, workspace, token_gate,
-               channel_gate, d_post_gamma, d_pre_gamma, d_token_gate, d_channel_gate)
+    _operands(("d_y", d_y, bf, shape), ("d_residual_out", d_residual_out, bf, shape), ("x", x, bf, shape),
+              ("residual", residual, bf, shape), ("post_gamma", post_gamma, bf, (H,)), ("pre_gamma", pre_gamma, bf, (H,)),
+              ("rstd", rstd, f32, (b, 2)), ("d_x", d_x, bf, shape), ("d_residual", d_residual, bf, shape),
+              ("workspace", workspace, workspace.dtype, workspace.shape), ("token_gate", token_gate, f32, (b,)),
+              ("channel_gate", channel_gate, bf, (H,)), ("d_post_gamma", d_post_gamma, f32, (H,)),
+              ("d_pre_gamma", d_pre_gamma, f32, (H,)), ("d_token_gate", d_token_gate, f32, (b,)),
+              ("d_channel_gate", d_channel_gate, f32, (H,)))
     _check("moe_tail_block_norm_grad", lib().moe_tail_block_norm_grad(
         _p(d_y), _p(d_residual_out), _p(x), _p(residual), _p(post_gamma), _p(pre_gamma), _p(token_gate), _p(channel_gate),
         _p(rstd), residual_scale, gain_center, b, H, _p(d_x), _p(d_residual), _p(d_post_gamma), _p(d_pre_gamma),
@@ -679,14 +676,10 @@ def _product_i4(name, x, w, group_scale, channel_scale, out, group, expert_offse
         raise ValueError(f"group must be one of {I4_GROUPS}, got {group}")
     if channels % halves:
         raise ValueError(f"w must have an even number of channels (gate and up), got shape {tuple(w.shape)}")
-    _like("x", x, torch.bfloat16, (rows, D))
-    _like("w", w, torch.uint8, (E, channels, -(-D // 128) * 64))
-    _like("group_scale", group_scale, torch.float8_e4m3fn, (E, channels, -(-(-(-D // group)) // 4) * 4))
-    _like("channel_scale", channel_scale, torch.float32, (E, channels))
-    if expert_offsets is not None:
-        _like("expert_offsets", expert_offsets, torch.int32, (E + 1,))
-    _like("out", out, torch.bfloat16, (rows, channels // halves))
-    _cuda_here(x, w, group_scale, channel_scale, expert_offsets, out)
+    _operands(("x", x, torch.bfloat16, (rows, D)), ("w", w, torch.uint8, (E, channels, -(-D // 128) * 64)),
+              ("group_scale", group_scale, torch.float8_e4m3fn, (E, channels, -(-(-(-D // group)) // 4) * 4)),
+              ("channel_scale", channel_scale, torch.float32, (E, channels)),
+              ("expert_offsets", expert_offsets, torch.int32, (E + 1,)), ("out", out, torch.bfloat16, (rows, channels // halves)))
     _check(name, getattr(lib(), name)(
         _p(x), _p(w), _p(group_scale), _p(channel_scale), _p(expert_offsets), rows, E, channels // halves, D, group, _p(out),
         _stream(stream)))

@@ -143,7 +143,7 @@ constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
 constexpr int kGroupColumns = 2048;  // of a row that shares its thread block with others
 constexpr int kMaxCluster = 8;       // thread blocks of a row: 32768 columns, eight a thread
 constexpr int kMaxGradBlocks = 160;
-constexpr int kLeastWarps = 4;       // one for each tensor of a row in shared memory
+constexpr int kAloneBytes = 116 * 1024;    // of which an SM has room for one thread block: two on one would leave others idle
 constexpr int kStagedBytes = 200 * 1024;  // of rows in shared memory
 
 // How a call's rows lie on thread blocks.
@@ -383,17 +383,22 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_
                "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32x2(uint32_t addr, float a, float b) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+// Two values into shared memory of a thread block of the cluster, counted by a barrier there.
+__device__ __forceinline__ void st_async_f32x2(uint32_t addr, float a, float b, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar)
+               : "memory");
 }
 
 // Wider rows: a row's (or a cluster's part of a row's) x, residual, d_y and d_residual_out arrive in shared memory, several
-// rows ahead, and each row has one barrier: the second sum of a row and the first of the next meet at it.
+// rows ahead, and each row has one barrier: the second sum of a row and the first of the next meet at it.  In a cluster the
+// warps send their sums to every thread block of it, and a barrier there counts their bytes: a barrier of the whole cluster
+// would also wait for the row's results on their way to memory (8192 columns: 5.5 us a row).
 template <bool POST, bool CHANNEL, bool CLUSTER>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const BlockNormGradArgs a, const GradShape s) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float2 s_sum[2][kMaxCluster * kGradWarps];
-  __shared__ __align__(8) uint64_t s_bar[8];
+  __shared__ __align__(8) uint64_t s_bar[8], s_sent[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = CLUSTER ? (int)cluster_rank() : 0, ranks = CLUSTER ? (int)cluster_size() : 1;
   const int64_t set = CLUSTER ? blockIdx.x / ranks : blockIdx.x;
@@ -402,6 +407,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
   const int tensors = a.d_residual_out ? 4 : 3;
   if (threadIdx.x == 0) {
     for (int i = 0; i < s.stages; ++i) mbar_init(bars + 8 * i, tensors);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(s_sent + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (CLUSTER) cluster_sync_all();  // its thread blocks have started, so that their shared memory can be written
@@ -433,11 +439,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
   Columns<POST, CHANNEL> columns;
   columns.load(a, first + v, live);
   Sums<POST, CHANNEL> sums;
-  auto wait = [&](uint32_t stage, uint32_t parity) {
-    if (!mbar_wait(bars + 8 * stage, parity)) atomicOr(&g_norm_error, kErrWaitFull);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity)) atomicOr(&g_norm_error, kErrWaitFull);
   };
   // Two sums over the row, the same in every thread, in a fixed order; slots in turn as for the groups.
   int slot = 0;
+  uint32_t sent_parity = 0;
   auto row_sums = [&](float x, float y) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -445,8 +452,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
       y += __shfl_xor_sync(0xffffffffu, y, off);
     }
     if (CLUSTER) {
-      if (lane < ranks) st_cluster_f32x2(map_to_rank(smem_addr(&s_sum[slot][part * kGradWarps + warp]), lane), x, y);
-      cluster_sync_all();
+      // A warp sends again after it has read what came for this row, so that a slot is never overtaken.
+      const uint32_t bar = smem_addr(s_sent + slot);
+      if (threadIdx.x == 0) mbar_expect_tx(bar, 8u * ranks * s.warps);
+      if (lane < ranks)
+        st_async_f32x2(map_to_rank(smem_addr(&s_sum[slot][part * kGradWarps + warp]), lane), x, y, map_to_rank(bar, lane));
+      wait(bar, sent_parity);
+      if (slot == 1) sent_parity ^= 1u;
     } else {
       if (lane == 0) s_sum[slot][warp] = make_float2(x, y);
       __syncthreads();
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
     const float dot = w.form(a, row, columns, ld_shared_v4(at), ld_shared_v4(at + apart), ld_shared_v4(at + 2 * apart));
     return live ? dot : 0.0f;
   };
-  wait(0, 0);
+  wait(bars, 0);
   float mean = row_sums(0.0f, form(r, mine)).y * a.rcpH;
   uint32_t stage = 0, parity = 0, at = mine;
   uint16_t *d_x = a.d_x + set * a.H + 8 * (first + v), *d_residual = a.d_residual + set * a.H + 8 * (first + v);
@@ -510,7 +522,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
     float dot_next = 0.0f;
     if (k + 1 < rows) {
       r = row_at(k + 1);
-      wait(stage, parity);
+      wait(bars + 8 * stage, parity);
       dot_next = form(r, at);
     }
     const float2 both = row_sums(dot, dot_next);
@@ -624,7 +636,10 @@ cudaError_t launch_grad(const BlockNormGradArgs& a, int most, int* sets, cudaStr
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(32 * s.warps * s.groups);  // every thread takes part in a row: its barriers count them all
-    cfg.dynamicSmemBytes = s.stages ? (size_t)s.stages * 64 * s.vectors + 512 : 0;  // threads past the last vector read on
+    if (s.stages) {
+      const int bytes = s.stages * 64 * s.vectors + 512;  // threads past the last vector read on
+      cfg.dynamicSmemBytes = bytes < kAloneBytes ? kAloneBytes : bytes;
+    }
   };
   shape(s.cluster);
   auto kernel = s.stages == 0 ? grad_groups_kernel<POST, CHANNEL>
@@ -637,13 +652,15 @@ cudaError_t launch_grad(const BlockNormGradArgs& a, int most, int* sets, cudaStr
   int at_once = most / s.cluster;
   if (s.cluster > 1) {  // the size of which the most SMs have a thread block
     int best = s.cluster, best_blocks = 0;
-    for (int c = s.cluster; c <= kMaxCluster && a.H >= 8 * 32 * kLeastWarps * c; ++c) {
+    // Only even sizes: of five, the clusters that should fit did not all run at once (1820 rows of 18432 columns: 128 us
+    // with five, 90 with six).  At least a warp for each tensor of a row.
+    for (int c = s.cluster + s.cluster % 2; c <= kMaxCluster && a.H >= 8 * 32 * 4 * c; c += 2) {
       shape(c);
-      const int n = clusters_at_once((const void*)kernel, cfg, c);
+      const int fit = clusters_at_once((const void*)kernel, cfg, c), n = fit < most / c ? fit : most / c;
       if (n * c > best_blocks) {
         best = c;
         best_blocks = n * c;
-        at_once = n < most / c ? n : most / c;
+        at_once = n;
       }
     }
     shape(best);
