@@ -213,12 +213,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) scales[j][h] = ahead[j][h] >> (8 * (block * kPer & 3));
-      load_scales(q, block + kWarps, ahead);
       if (ok && !warp_wait(full + 8 * ring.slot, ring.parity, abort_ptr, limit)) {
         if (lane == 0) give_up(kErrWaitFull);
         ok = false;
       }
       if (!ok) continue;  // the tiles are walked to the end: the warps meet at barriers
+      load_scales(q, block + kWarps, ahead);  // not before a wait: that would wait for them too
       if (block < a.blocks) {
         const uint32_t w = base + ring.slot * kStage + warp * 64 + 16 * t;
         const uint32_t x = base + ring.slot * kStage + kWeights + warp * kXBlock + x_row * 128;

@@ -27,6 +27,7 @@ __device__ __forceinline__ void raise_error(unsigned bit) { atomicOr(&g_i4_tiles
 
 constexpr int kRun = 16;                  // accumulator columns (rows of the result) written at a time
 constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
+constexpr int kTileRing = 32;             // tiles that the weights' warp has described: more than it can be ahead
 
 // The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them (two MMAs for the same rows: with
 // many rows it is the rows' way from L2 that bounds, and this halves it).
@@ -77,7 +78,6 @@ struct Args {
 // A tile: `rows` rows from r0 by channels from n0 (of the result) of expert e.
 struct Tile {
   int e, n0, r0, rows;
-  bool shared;  // more than one row tile reads these weights
 };
 
 template <class F, int GROUP, bool GATED>
@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort
   volatile uint32_t* abort_ptr = word + 1;
   const uint32_t slot = at;
-  int32_t* s_first = reinterpret_cast<int32_t*>(base_ptr + (at - base) + 16);  // [E + 1] row tiles before an expert
+  Tile* s_tile = reinterpret_cast<Tile*>(base_ptr + (at - base) + 16);
+  int32_t* s_first = reinterpret_cast<int32_t*>(s_tile + kTileRing);           // [E + 1] row tiles before an expert
   int32_t* s_row = s_first + a.E + 1;                                           // [E] its first row
   int32_t* s_count = s_row + a.E;                                               // [E] its rows
 
@@ -165,7 +166,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
 
   const int n_tiles = (a.N + kOut - 1) / kOut;
   const int64_t tiles = (int64_t)s_first[a.E] * n_tiles;
-  auto tile_at = [&](int64_t i, Tile& q) {  // in the order (expert, channel tile, row tile)
+  // Tiles in the order (expert, channel tile, row tile).  Finding one takes a thousand cycles: the warps that have none to
+  // spare, those that convert and the one that issues MMAs, take it from the ring where the weights' warp leaves it; its
+  // weights' arrival tells that it is there.
+  auto tile_at = [&](int64_t i, Tile& q, bool* again = nullptr) {
     if (i >= tiles) return false;
     const int e = expert_of_tile(s_first, a.E, n_tiles, i);
     const int row_tiles = s_first[e + 1] - s_first[e];
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     const int share = ((s_count[e] + row_tiles - 1) / row_tiles + 15) & ~15;
     q.r0 = s_row[e] + t * share;
     q.rows = min(share, s_count[e] - t * share);  // at least one: NT * (row_tiles - 1) < s_count
-    q.shared = row_tiles > 1;
+    if (again) *again = row_tiles > 1;  // more than one row tile reads these weights
     return true;
   };
   const int pairs = (a.blocks + 1) / 2;  // an odd last block has one of zeros beside it
@@ -193,10 +197,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     const uint64_t once = policy_evict_first(), again = policy_evict_last();
     int64_t g = 0;
     Ring w;
-    bool ok = true;
+    bool ok = true, shared = false;
     Tile q;
-    for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
-      const uint64_t policy = q.shared ? again : once;
+    int k = 0;
+    for (int64_t i = blockIdx.x; ok && tile_at(i, q, &shared); i += gridDim.x, ++k) {
+      const uint64_t policy = shared ? again : once;
+      if (lane == 0) s_tile[k % kTileRing] = q;
+      __syncwarp();
       for (int b = 0; b < pairs; ++b, ++g, w.step(a.w_stages)) {
         if (!warp_wait(w_empty + 8 * w.slot, w.parity ^ 1u, abort_ptr)) {  // the first round finds it free
           if (lane == 0) give_up(kErrWaitEmpty);
@@ -258,14 +265,24 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     const unsigned long long limit = a.stage_wait_ns ? a.stage_wait_ns : kWaitLimitNs;
     Ring x, s, acc;
     bool ok = true;
-    Tile q;
-    for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x, acc.step(kAccs)) {
+    int k = 0;
+    for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++k, acc.step(kAccs)) {
       if (!warp_wait(acc_empty + 8 * acc.slot, acc.parity ^ 1u, abort_ptr)) {
         if (lane == 0) give_up(kErrWaitAccum);
         break;
       }
-      const uint32_t idesc = idesc_bf16(128, (q.rows + 15) & ~15);
       const uint32_t d = tmem + acc.slot * (kSubs * NT);
+      Tile q = {};
+      if (k == 0) {
+        tile_at(blockIdx.x, q);
+      } else {  // once its first step is there
+        if (!warp_wait(step_full + 8 * s.slot, s.parity, abort_ptr, limit)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          break;
+        }
+        q = s_tile[k % kTileRing];
+      }
+      const uint32_t idesc = idesc_bf16(128, (q.rows + 15) & ~15);
       const int steps = kStepsOfPair * pairs;
       for (int b = 0; b < steps; ++b, s.step(kSlots)) {
         if (!warp_wait(step_full + 8 * s.slot, s.parity, abort_ptr, limit)) {
@@ -321,8 +338,19 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     s.step(kSlots, set);
     x.step(kXStages, set);
     bool ok = true, second_round = false;
-    Tile q;
-    for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
+    int k = 0;
+    for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++k) {
+      Tile q = {};
+      if (k == 0) {  // found here, and its scales asked for while its weights are on their way
+        tile_at(blockIdx.x, q);
+      } else if (ahead < pairs) {
+        if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
+          break;
+        }
+        q = s_tile[k % kTileRing];
+      }
       // this thread's channel; past the last: the last
       const int n = min(q.n0 + (GATED ? row % kHalf : row), a.N - 1) + (GATED && row >= kHalf ? a.N : 0);
       const uint8_t* scales = a.group_scale + ((int64_t)q.e * channels + n) * a.pitch;
@@ -330,11 +358,16 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         const int first = (2 * pair + first_block) * kPer & ~3;
 #pragma unroll
         for (int k = 0; k < kWords; ++k)
-          to[k] = first + 4 * k < a.groups ? __ldg(reinterpret_cast<const uint32_t*>(scales + first + 4 * k)) : 0u;
+          to[k] = pair < pairs && first + 4 * k < a.groups ? __ldg(reinterpret_cast<const uint32_t*>(scales + first + 4 * k)) : 0u;
       };
       uint32_t next[kWords];
       load_scales(ahead, next);
       for (; ahead < pairs; ahead += kStride, w.step(a.w_stages, kStride)) {
+        if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
+          if (lane == 0) give_up(kErrWaitFull);
+          ok = false;
+          break;
+        }
         const int first = (2 * ahead + first_block) * kPer;  // group
         uint32_t gs[kWords];
 #pragma unroll
@@ -344,12 +377,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
           if (left < 4) gs[k] &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
         }
         if (kGroups < 4) gs[0] >>= 8 * (first & 3);
-        load_scales(ahead + kStride, next);
-        if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
-          if (lane == 0) give_up(kErrWaitFull);
-          ok = false;
-          break;
-        }
+        load_scales(ahead + kStride, next);  // not before a wait: that would wait for them too
         Factors f;
         uint4 v[4];  // words 4 t + i: columns 32 i + 8 t .. of a block
 #pragma unroll
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     const int reader = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const int channels = GATED ? 2 * a.N : a.N;
     // this thread's channel of the result, and from which accumulator, of the tile's first
-    const int mine = WIDE ? row + (GATED ? 0 : 128 * reader) : GATED ? row & 63 : row;
+    const int column = WIDE ? row + (GATED ? 0 : 128 * reader) : GATED ? row & 63 : row;
     auto value = [](uint32_t bits) { return __uint_as_float(bits); };
     // 16 rows of 128 channels (of a narrow gated tile, 64) of this set, as they lie in shared memory, to the result
     auto store = [&](const Tile& q, int c, int n0, auto eight) {
@@ -428,8 +456,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     bool ok = true;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x, acc.step(kAccs)) {
-      const float* cs_at = a.channel_scale + (int64_t)q.e * channels + q.n0 + mine;
-      const bool there = q.n0 + mine < a.N;
+      const float* cs_at = a.channel_scale + (int64_t)q.e * channels + q.n0 + column;
+      const bool there = q.n0 + column < a.N;
       const float cs = there ? kScaled * __ldg(cs_at + (GATED && !WIDE && row >= 64 ? a.N : 0)) : 0.0f;
       const float cs_up = GATED && WIDE && there ? kScaled * __ldg(cs_at + a.N) : 0.0f;
       ok = warp_wait(acc_full + 8 * acc.slot, acc.parity, abort_ptr);
@@ -547,7 +575,7 @@ cudaError_t launch_form(const ProductI4Args& p, const CUtensorMap& map_w, const 
   a.groups = (p.D + GROUP - 1) / GROUP;
   a.pitch = (a.groups + 3) / 4 * 4;
   a.stage_wait_ns = stage_wait_limit_ns();
-  const int fixed = 1024 + F::kReaders * kStaging + 8 * (2 * 12 + 2 * 6 + 2 * 4 + 2 * 2 + 1) + 32 + 4 * (3 * p.E + 1);
+  const int fixed = 1024 + F::kReaders * kStaging + 8 * (2 * 12 + 2 * 6 + 2 * 4 + 2 * 2 + 1) + 32 + kTileRing * 16 + 4 * (3 * p.E + 1);
   a.w_stages = (kLimit - fixed - kXRing) / F::kWStage;
   if (a.w_stages > 12) a.w_stages = 12;
   // A set of converting warps that takes every third pair must meet the same slots in every round: else it could ask for
