@@ -58,6 +58,7 @@ constexpr int kChannels = 32;                   // stored ones of a tile: two MM
 constexpr int kRowBytes = kWarps * 64;          // of a channel in a stage: a block for each warp
 constexpr int kWeights = kChannels * kRowBytes, kXBlock = kRows * 256, kStage = kWeights + kWarps * kXBlock;
 constexpr int kStages = 3;                      // 96 KB: two thread blocks an SM
+constexpr int kWideFrom = 256;                  // rows for an expert from which wide tiles pay
 constexpr int kMostExperts = 256;               // whose rows fit shared memory beside the stages
 constexpr int kPadded = 40;                     // floats of a row of a warp's 32 channels: no two lanes in one bank
 
@@ -314,13 +315,13 @@ ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sm
   p.tiles = want > kRows || hit * ((N + 127) / 128) * (gated ? 2 : 1) >= sms / 2 || E > kMostExperts;
   p.wide = false;
   if (p.tiles) {
-    p.rows = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
-    const int64_t row_tiles = E == 1 ? (R + 127) / 128 : R / 128 + hit;
-    p.wide = want > 128 && row_tiles * ((N + 255) / 256) * (gated ? 2 : 1) >= sms;
+    const int64_t row_tiles = E == 1 ? (R + 127) / 128 : R / 128 + hit;  // of a wide tile's rows
+    p.wide = want > kWideFrom && row_tiles * ((N + 255) / 256) * (gated ? 2 : 1) >= sms;
+    p.rows = p.wide ? 128 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
     p.box_columns = 128;
     p.box_channels = (gated ? 64 : 128) * (p.wide ? 2 : 1);
-    p.box_rows = p.rows < 64 ? p.rows : 64;
-    p.box_chunks = D % 64 ? 0 : p.rows > 64 ? 1 : 4;
+    p.box_rows = p.wide ? 64 : p.rows;
+    p.box_chunks = D % 64 ? 0 : p.wide ? 1 : 4;
   } else {
     p.rows = kRows;
     p.box_columns = kRowBytes;

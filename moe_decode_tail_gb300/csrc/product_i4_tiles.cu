@@ -600,8 +600,7 @@ cudaError_t launch_rows(const ProductI4Args& p, const ProductI4Plan& plan, const
   switch (plan.rows) {
     case 16: return launch_form<Form<16, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
     case 32: return launch_form<Form<32, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    case 64: return launch_form<Form<64, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
-    default: return launch_form<Form<128, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
+    default: return launch_form<Form<64, false>, GROUP, GATED>(p, map_w, map_x, sms, stream);
   }
 }
 
