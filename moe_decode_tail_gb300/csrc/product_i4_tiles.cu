@@ -1,16 +1,22 @@
-// The 4-bit product on the 5th-generation tensor cores (sm_103a): tiles of 128 channels by 16 to 256 rows.
+// The 4-bit product on the 5th-generation tensor cores (sm_103a): tiles of 128 channels by up to 64 rows, or of 256 by 128.
 //
-// Persistent, one thread block an SM.  The packed weights cross memory once, by TMA (128 channels x 128 bytes, 256 columns of
-// the reduction: a pair of blocks); converting warps, a block of 32 channels each, turn them into BF16 in registers, their
-// groups' scales multiplied in, and store them into tensor memory, from where the MMA takes its A operand (a thread's
-// channel is a TMEM lane, so nothing is shuffled or written back to shared memory).  The rows arrive by TMA as the B operand;
-// four warps (eight at 256 rows) read finished accumulators, scale them by channel and write BF16.  The weight stream runs
-// on across tiles.
+// Persistent, one thread block an SM.  The packed weights cross memory once, by TMA (128 bytes of a channel, 256 columns of
+// the reduction: a pair of blocks); converting warps, 32 channels each, turn them into BF16 in registers, their groups' scales
+// multiplied in, and store them into tensor memory, from where the MMA takes its A operand (a thread's channel is a TMEM lane,
+// so nothing is shuffled or written back to shared memory).  The rows arrive by TMA as the B operand; epilogue warps read
+// finished accumulators, scale them by channel and write BF16.  The weight stream runs on across tiles.
 //
-// A gated tile has 64 gate channels, then the 64 up channels that go with them; they meet in shared memory.
+// A gated tile has its gate channels, then the up channels that go with them.  In a narrow one they are in one accumulator
+// and meet in shared memory; a wide one has an accumulator for each, and a thread both factors of a result.
 //
-// What a step costs the MMA warp besides its MMAs bounds the weight stream with few rows, so that a step is a whole pair then,
-// with one barrier to wait for and one commit (a block a step, two barriers and commits: 570 cycles for 8 KB, 3.3 TB/s).
+// With few rows the weights' way from memory is the bound, and before it what a step costs the warps that issue MMAs and that
+// convert.  64 tokens x 8 routes over 128 experts of 2048 x 4096 take 94 us (0.54 GB, 0.87 of the measured copy rate), of
+// 4096 x 1024 with groups of 32 columns 59 us (0.73).  On the way there: a block a step with two barriers and commits 180 us;
+// a pair a step, one barrier and one commit 112; three sets of converting warps that take whole steps instead of two that
+// share them 102; rows asked for further ahead 100; tiles found by one warp for those that have no time to 94.
+// With many rows the rows' way from L2 counts (every tile of channels reads them again) and the MMAs: 32768 rows over 128
+// experts of 4096 x 2048 take 465 us, 1.2 PFLOP/s (0.62 of a library BF16 product); tiles of 128 channels by 256 rows took 467
+// and such of 128 by 128 rows 557.  The MMA with A in tensor memory has taken a third more cycles than its operations here.
 //
 // Every wait is bounded in time; on expiry the kernel raises a bit in the device error word, lets its copies and MMAs
 // finish, frees its tensor memory and returns.
@@ -29,22 +35,22 @@ constexpr int kRun = 16;                  // accumulator columns (rows of the re
 constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
 constexpr int kTileRing = 32;             // tiles that the weights' warp has described: more than it can be ahead
 
-// The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them (two MMAs for the same rows: with
-// many rows it is the rows' way from L2 that bounds, and this halves it).
+// The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them: two MMAs for the same rows, whose
+// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 90 us, 106 without).
 template <int NT_, bool WIDE_>
 struct Form {
   static constexpr int NT = NT_;
   static constexpr bool WIDE = WIDE_;
   static constexpr int kSubs = WIDE ? 2 : 1;                        // tiles of 128 stored channels, the MMA's M
   static constexpr int kWStage = kSubs * 128 * 128;                 // bytes of a pair of blocks of them
-  static constexpr int kBlocks = NT > 64 ? 1 : 2;                   // of a step of the MMA warp
+  static constexpr int kBlocks = WIDE ? 1 : 2;                      // of a step of the MMA warp
   static constexpr int kStepsOfPair = 2 / kBlocks;
   static constexpr int kSlotColumns = 64 * kBlocks * kSubs;         // of a step's A in tensor memory: two BF16 each
   static constexpr int kAccs = WIDE ? 1 : 2;                        // accumulators, taken in turn
   static constexpr int kTmemA = kAccs * kSubs * NT;                 // first column of the A ring
   static constexpr int kSlots = (512 - kTmemA) / kSlotColumns;      // steps in it
-  // Sets of converting warps take the steps in turn, a warp for 32 channels.
-  static constexpr int kSets = WIDE ? 1 : NT > 64 ? 2 : 3;
+  // Sets of converting warps take the pairs in turn, a warp for 32 channels.
+  static constexpr int kSets = WIDE ? 1 : 3;
   static constexpr int kSetWarps = 4 * kSubs;
   static constexpr int kReaders = WIDE ? 2 : 1;                     // sets of four epilogue warps (one accumulator: it waits)
   static constexpr int kEpilogueWarps = 4 * kReaders;
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
   if (warp == 0) {
     for (int s = lane; s < a.w_stages; s += 32) {
       mbar_init(w_full + 8 * s, 1);
-      mbar_init(w_empty + 8 * s, kBlocks == 2 ? kSetWarps : kSets * kSetWarps);  // one set reads it, or all of them
+      mbar_init(w_empty + 8 * s, kSetWarps);  // one set reads it
     }
     for (int s = lane; s < kXStages; s += 32) {
       mbar_init(x_full + 8 * s, 1);
@@ -324,16 +330,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     __syncwarp();
   } else if (warp >= kEpilogueWarps) {
     // ---------------- 4 bits to BF16, one TMEM lane a thread ----------------
-    // Set s takes the steps s, s + kSets, ... of the stream: pairs, or one block of each (two sets), or both in turn (one).
+    // Set s takes the pairs s, s + kSets, ... of the stream, a step each, or two (wide).
     const int set = (warp - kEpilogueWarps) / kSetWarps, sub = (warp - kEpilogueWarps) % kSetWarps >> 2, quarter = warp & 3;
     const int row = sub * 128 + quarter * 32 + lane;   // of the staged tile
     const int channels = GATED ? 2 * a.N : a.N;
-    constexpr int kStride = kBlocks == 2 ? kSets : 1;  // pairs from one of a set to its next
-    constexpr int kMine = kBlocks == 2 ? 1 : 2 / kSets;  // steps of a pair
-    constexpr int kGroups = kPer * kBlocks * kMine, kWords = (kGroups + 3) / 4;  // of these: their scales, in words of four
-    const int first_block = kBlocks == 1 && kSets == 2 ? set : 0;                // of a pair
+    constexpr int kGroups = 2 * kPer, kWords = (kGroups + 3) / 4;  // of a pair: their scales, in words of four
     Ring w, s, x;
-    int ahead = kBlocks == 2 ? set : 0;                // pairs until this set's next one
+    int ahead = set;  // pairs until this set's next one
     w.step(a.w_stages, ahead);
     s.step(kSlots, set);
     x.step(kXStages, set);
@@ -354,21 +357,21 @@ __global__ void __launch_bounds__(F::kThreads, 1)
       // this thread's channel; past the last: the last
       const int n = min(q.n0 + (GATED ? row % kHalf : row), a.N - 1) + (GATED && row >= kHalf ? a.N : 0);
       const uint8_t* scales = a.group_scale + ((int64_t)q.e * channels + n) * a.pitch;
-      auto load_scales = [&](int pair, uint32_t (&to)[kWords]) {  // the words with those of its steps
-        const int first = (2 * pair + first_block) * kPer & ~3;
+      auto load_scales = [&](int pair, uint32_t (&to)[kWords]) {  // the words with those of a pair
+        const int first = pair * kGroups & ~3;
 #pragma unroll
         for (int k = 0; k < kWords; ++k)
           to[k] = pair < pairs && first + 4 * k < a.groups ? __ldg(reinterpret_cast<const uint32_t*>(scales + first + 4 * k)) : 0u;
       };
       uint32_t next[kWords];
       load_scales(ahead, next);
-      for (; ahead < pairs; ahead += kStride, w.step(a.w_stages, kStride)) {
+      for (; ahead < pairs; ahead += kSets, w.step(a.w_stages, kSets)) {
         if (!warp_wait(w_full + 8 * w.slot, w.parity, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
           break;
         }
-        const int first = (2 * ahead + first_block) * kPer;  // group
+        const int first = ahead * kGroups;  // group
         uint32_t gs[kWords];
 #pragma unroll
         for (int k = 0; k < kWords; ++k) {
@@ -377,18 +380,18 @@ __global__ void __launch_bounds__(F::kThreads, 1)
           if (left < 4) gs[k] &= left > 0 ? (1u << (8 * left)) - 1u : 0u;
         }
         if (kGroups < 4) gs[0] >>= 8 * (first & 3);
-        load_scales(ahead + kStride, next);  // not before a wait: that would wait for them too
+        load_scales(ahead + kSets, next);  // not before a wait: that would wait for them too
         Factors f;
         uint4 v[4];  // words 4 t + i: columns 32 i + 8 t .. of a block
 #pragma unroll
-        for (int step = 0; step < kMine; ++step, s.step(kSlots, kSets), x.step(kXStages, kSets)) {
+        for (int step = 0; step < kStepsOfPair; ++step, s.step(kSlots, kSets), x.step(kXStages, kSets)) {
           const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + s.slot * kSlotColumns + sub * 64 * kBlocks;
 #pragma unroll
           for (int h = 0; h < 2 * kBlocks; ++h) {  // 64 columns
             if (h % 2 == 0) {
 #pragma unroll
               for (int t = 0; t < 4; ++t)
-                v[t] = ld_shared_v4(w_ring + w.slot * kWStage + sw128_offset(row, 4 * (first_block + step + h / 2) + t));
+                v[t] = ld_shared_v4(w_ring + w.slot * kWStage + sw128_offset(row, 4 * (step + h / 2) + t));
             }
             uint32_t r[32];
 #pragma unroll
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
-          if (step == kMine - 1 && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
+          if (step == kStepsOfPair - 1 && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
           // one warp of the set sees the rows arrive too, so that the MMA warp has one barrier to wait for
           if (kJoint && quarter == 0 && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr)) {
             if (lane == 0) give_up(kErrWaitFull);
@@ -581,7 +584,7 @@ cudaError_t launch_form(const ProductI4Args& p, const CUtensorMap& map_w, const 
   // A set of converting warps that takes every third pair must meet the same slots in every round: else it could ask for
   // a slot's next round while another set's copy in it is still on its way, and the parity of the round before would tell
   // it that its own had landed.
-  if (F::kBlocks == 2) a.w_stages -= a.w_stages % F::kSets;
+  a.w_stages -= a.w_stages % F::kSets;
   a.whole = p.D % 64 == 0;
   auto kernel = product_i4_tiles_kernel<F, GROUP, GATED>;
   cudaError_t e = ensure_smem_limit((const void*)kernel, kLimit);
