@@ -582,14 +582,13 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, int sms, cudaStream_t stre
   auto launch = [&](auto kernel, int vpt) {
     return launch_pdl(kernel, dim3(a.b), dim3(threads_for(nv, vpt)), 0, stream, a);
   };
-  const int vpt = vectors_for(nv, a.b, sms, 2);
+  // 16384 rows of 4096: 86.8 us with four vectors a thread, 92.5 with two, 102 with one.
+  const int vpt = vectors_for(nv, a.b, sms, 4);
   if (a.post_gamma)
     return vpt == 1   ? launch(block_norm_kernel<true, 1>, 1)
-           : vpt == 2 ? launch(block_norm_kernel<true, 2>, 2)
            : vpt == 4 ? launch(block_norm_kernel<true, 4>, 4)
                       : launch(block_norm_kernel<true, 8>, 8);
   return vpt == 1   ? launch(block_norm_kernel<false, 1>, 1)
-         : vpt == 2 ? launch(block_norm_kernel<false, 2>, 2)
          : vpt == 4 ? launch(block_norm_kernel<false, 4>, 4)
                     : launch(block_norm_kernel<false, 8>, 8);
 }

@@ -320,7 +320,7 @@ ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sm
     p.rows = p.wide ? 128 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
     p.box_columns = 128;
     p.box_channels = (gated ? 64 : 128) * (p.wide ? 2 : 1);
-    p.box_rows = p.wide ? 64 : p.rows;
+    p.box_rows = p.rows;
     p.box_chunks = D % 64 ? 0 : p.wide ? 1 : 4;
   } else {
     p.rows = kRows;

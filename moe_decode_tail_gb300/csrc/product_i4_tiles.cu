@@ -63,7 +63,6 @@ struct Form {
   static constexpr int kXColumns = kJoint ? 128 * kBlocks : 64;
   static constexpr int kXStages = kRelayed ? 2 * kSlots : kJoint ? kSlots : 6;
   static constexpr int kXHalf = NT * 128, kXStage = NT * kXColumns * 2;  // bytes of 64 columns, and of a stage
-  static constexpr int kBox = NT < 64 ? NT : 64;                    // rows of one TMA box
   static_assert(kSlots % kSets == 0, "a set meets the same slots in every round");
 };
 
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
   constexpr int kSlotColumns = F::kSlotColumns, kAccs = F::kAccs, kTmemA = F::kTmemA, kSlots = F::kSlots, kSets = F::kSets;
   constexpr int kSetWarps = F::kSetWarps, kReaders = F::kReaders, kEpilogueWarps = F::kEpilogueWarps;
   constexpr int kThreads = F::kThreads, kXColumns = F::kXColumns, kXStages = F::kXStages, kXHalf = F::kXHalf;
-  constexpr int kXStage = F::kXStage, kBox = F::kBox;
+  constexpr int kXStage = F::kXStage;
   constexpr bool WIDE = F::WIDE, kJoint = F::kJoint, kRelayed = F::kRelayed;
   constexpr int kWarpW = kEpilogueWarps + kSets * kSetWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
   constexpr int kXOfStep = 128 * kBlocks / kXColumns;
@@ -237,7 +236,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     bool ok = true;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
-      const int boxes = NT <= kBox ? 1 : (q.rows + kBox - 1) / kBox;
       for (int b = 0; b < kXOfStep * kStepsOfPair * pairs; ++b, ++g, x.step(kXStages)) {
         if (!warp_wait(x_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
@@ -246,17 +244,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         }
         if (elect_one()) {
           const uint32_t dst = x_ring + x.slot * kXStage, bar = x_full + 8 * x.slot;
-          mbar_expect_tx(bar, (uint32_t)(kXColumns / 64 * boxes * kBox * 128));
-          if (a.whole && kBox == NT) {
+          mbar_expect_tx(bar, kXStage);
+          if (a.whole) {
             tma_load_3d(dst, &map_x, bar, 0, q.r0, kXColumns / 64 * b, keep);
           } else {
 #pragma unroll
             for (int h = 0; h < kXColumns / 64; ++h)
-              for (int c = 0; c < boxes; ++c) {
-                const uint32_t to = dst + h * kXHalf + c * kBox * 128;
-                if (a.whole) tma_load_3d(to, &map_x, bar, 0, q.r0 + c * kBox, kXColumns / 64 * b + h, keep);
-                else tma_load_2d(to, &map_x, bar, kXColumns * b + 64 * h, q.r0 + c * kBox, keep);
-              }
+              tma_load_2d(dst + h * kXHalf, &map_x, bar, kXColumns * b + 64 * h, q.r0, keep);
           }
         }
         __syncwarp();
