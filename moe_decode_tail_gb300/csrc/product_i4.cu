@@ -321,7 +321,7 @@ ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sm
     p.box_columns = 128;
     p.box_channels = (gated ? 64 : 128) * (p.wide ? 2 : 1);
     p.box_rows = p.rows;
-    p.box_chunks = D % 64 ? 0 : p.wide ? 1 : 4;
+    p.box_chunks = D % 64 ? 0 : p.wide ? 2 : 4;
   } else {
     p.rows = kRows;
     p.box_columns = kRowBytes;

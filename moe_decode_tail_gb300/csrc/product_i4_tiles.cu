@@ -55,13 +55,12 @@ struct Form {
   static constexpr int kReaders = WIDE ? 2 : 1;                     // sets of four epilogue warps (one accumulator: it waits)
   static constexpr int kEpilogueWarps = 4 * kReaders;
   static constexpr int kThreads = 32 * (kEpilogueWarps + kSets * kSetWarps + 3);
-  // Rows of a wide tile come in stages of 64 columns, so that a stage is free again soon; the MMA warp waits for those
-  // itself and gives them back.  Others come a step at a time, and their arrival is seen by the converting warps.  Up to 32
-  // rows have twice as many slots as the step ring, so that their copy is asked for well before it is needed; the set that
-  // finds a step's slot free again passes that on.
-  static constexpr bool kJoint = !WIDE, kRelayed = NT <= 32;
-  static constexpr int kXColumns = kJoint ? 128 * kBlocks : 64;
-  static constexpr int kXStages = kRelayed ? 2 * kSlots : kJoint ? kSlots : 6;
+  // Rows come a step at a time, and their arrival is seen by the converting warps, so that the MMA warp has one barrier to
+  // wait for.  But for 64 rows (shared memory) they have twice as many slots as the step ring, so that their copy is asked
+  // for well before it is needed; the set that finds a step's slot free again passes that on.
+  static constexpr bool kRelayed = WIDE || NT <= 32;
+  static constexpr int kXColumns = 128 * kBlocks;
+  static constexpr int kXStages = kRelayed ? 2 * kSlots : kSlots;
   static constexpr int kXHalf = NT * 128, kXStage = NT * kXColumns * 2;  // bytes of 64 columns, and of a stage
   static_assert(kSlots % kSets == 0, "a set meets the same slots in every round");
 };
@@ -94,9 +93,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
   constexpr int kSetWarps = F::kSetWarps, kReaders = F::kReaders, kEpilogueWarps = F::kEpilogueWarps;
   constexpr int kThreads = F::kThreads, kXColumns = F::kXColumns, kXStages = F::kXStages, kXHalf = F::kXHalf;
   constexpr int kXStage = F::kXStage;
-  constexpr bool WIDE = F::WIDE, kJoint = F::kJoint, kRelayed = F::kRelayed;
+  constexpr bool WIDE = F::WIDE, kRelayed = F::kRelayed;
   constexpr int kWarpW = kEpilogueWarps + kSets * kSetWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
-  constexpr int kXOfStep = 128 * kBlocks / kXColumns;
   constexpr int kPer = 128 / GROUP;              // groups of a block
   constexpr int kHalf = 64 * kSubs;              // of a gated tile: gate channels, then up channels
   constexpr int kOut = GATED ? kHalf : 2 * kHalf;  // channels of the result of a tile
@@ -116,7 +114,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
   };
   const uint32_t w_full = bars(a.w_stages), w_empty = bars(a.w_stages), x_full = bars(kXStages);
   const uint32_t step_full = bars(kSlots), step_empty = bars(kSlots);
-  const uint32_t x_empty = kJoint && !kRelayed ? step_empty : bars(kXStages);
+  const uint32_t x_empty = kRelayed ? bars(kXStages) : step_empty;
   const uint32_t acc_full = bars(kAccs), acc_empty = bars(kAccs), mma_done = bars(1);
   at = (at + 15u) & ~15u;
   volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(base_ptr + (at - base));  // TMEM base, abort
@@ -134,7 +132,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     }
     for (int s = lane; s < kXStages; s += 32) {
       mbar_init(x_full + 8 * s, 1);
-      if (!kJoint || kRelayed) mbar_init(x_empty + 8 * s, 1);
+      if (kRelayed) mbar_init(x_empty + 8 * s, 1);
     }
     if (lane < kSlots) {
       mbar_init(step_full + 8 * lane, kSetWarps);
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     bool ok = true;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
-      for (int b = 0; b < kXOfStep * kStepsOfPair * pairs; ++b, ++g, x.step(kXStages)) {
+      for (int b = 0; b < kStepsOfPair * pairs; ++b, ++g, x.step(kXStages)) {
         if (!warp_wait(x_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
@@ -284,38 +282,26 @@ __global__ void __launch_bounds__(F::kThreads, 1)
       }
       const uint32_t idesc = idesc_bf16(128, (q.rows + 15) & ~15);
       const int steps = kStepsOfPair * pairs;
-      for (int b = 0; b < steps; ++b, s.step(kSlots)) {
+      for (int b = 0; b < steps; ++b, s.step(kSlots), x.step(kXStages)) {
         if (!warp_wait(step_full + 8 * s.slot, s.parity, abort_ptr, limit)) {
           if (lane == 0) give_up(kErrWaitFull);
           ok = false;
           break;
         }
+        tc_fence_after();
         const uint32_t w = tmem + kTmemA + s.slot * kSlotColumns;
+        const uint64_t bdesc = smem_desc_sw128(x_ring + x.slot * kXStage);
+        if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < kXOfStep; ++h, x.step(kXStages)) {
-          if (!kJoint && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr, limit)) {
-            if (lane == 0) give_up(kErrWaitFull);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bdesc = smem_desc_sw128(x_ring + x.slot * kXStage);
-          if (elect_one()) {
+          for (int kk = 0; kk < kXColumns / 16; ++kk)  // 16 columns: 8 TMEM columns of A, 32 bytes along B's swizzled row
 #pragma unroll
-            for (int kk = 0; kk < kXColumns / 16; ++kk)  // 16 columns: 8 TMEM columns of A, 32 bytes along B's swizzled row
-#pragma unroll
-              for (int m = 0; m < kSubs; ++m)
-                mma_ts(d + m * NT, w + 64 * kBlocks * m + 32 * h + 8 * kk, bdesc + (kk / 4) * (kXHalf >> 4) + 2 * (kk % 4), idesc,
-                       (b > 0 || h > 0 || kk > 0) ? 1u : 0u);
-            if (!kJoint) mma_commit(x_empty + 8 * x.slot);
-            if (h == kXOfStep - 1) {
-              mma_commit(step_empty + 8 * s.slot);
-              if (b == steps - 1) mma_commit(acc_full + 8 * acc.slot);
-            }
-          }
-          __syncwarp();
+            for (int m = 0; m < kSubs; ++m)
+              mma_ts(d + m * NT, w + 64 * kBlocks * m + 8 * kk, bdesc + (kk / 4) * (kXHalf >> 4) + 2 * (kk % 4), idesc,
+                     (b > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(step_empty + 8 * s.slot);
+          if (b == steps - 1) mma_commit(acc_full + 8 * acc.slot);
         }
-        if (!kJoint && !ok) break;
+        __syncwarp();
       }
     }
     if (elect_one()) mma_commit(mma_done);  // the MMAs that were issued are done before tensor memory is freed
@@ -334,7 +320,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     w.step(a.w_stages, ahead);
     s.step(kSlots, set);
     x.step(kXStages, set);
-    bool ok = true, second_round = false;
+    bool ok = true;
+    int fresh = kSlots / kSets;  // this set's slots that no step has had yet
     int k = 0;
     for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++k) {
       Tile q = {};
@@ -401,9 +388,9 @@ __global__ void __launch_bounds__(F::kThreads, 1)
               if (!ok) break;
               tc_fence_after();
               // the step that had this slot before is done, and so are its rows
-              if (kRelayed && second_round && quarter == 0 && lane == 0)
+              if (fresh > 0) --fresh;
+              else if (kRelayed && sub == 0 && quarter == 0 && lane == 0)
                 mbar_arrive(x_empty + 8 * (x.slot < kSlots ? x.slot + kSlots : x.slot - kSlots));
-              second_round = true;
             }
             tmem_st32(dst + 32 * h, r);
           }
@@ -417,7 +404,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
           // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
           if (step == kStepsOfPair - 1 && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
           // one warp of the set sees the rows arrive too, so that the MMA warp has one barrier to wait for
-          if (kJoint && quarter == 0 && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr)) {
+          if (sub == 0 && quarter == 0 && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr)) {
             if (lane == 0) give_up(kErrWaitFull);
             ok = false;
             break;

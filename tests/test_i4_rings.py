@@ -33,17 +33,16 @@ class Ring:
 
 
 FORMS = {  # as product_i4_tiles.cu has them
-    "16 and 32 rows": dict(blocks=2, slots=3, sets=3, accs=2, joint=True, relayed=True, x_stages=6, w_stages=9),
-    "64 rows": dict(blocks=2, slots=3, sets=3, accs=2, joint=True, relayed=False, x_stages=3, w_stages=6),
-    "wide": dict(blocks=1, slots=2, sets=1, accs=1, joint=False, relayed=False, x_stages=6, w_stages=3),
+    "16 and 32 rows": dict(blocks=2, slots=3, sets=3, accs=2, relayed=True, x_stages=6, w_stages=9),
+    "64 rows": dict(blocks=2, slots=3, sets=3, accs=2, relayed=False, x_stages=3, w_stages=6),
+    "wide": dict(blocks=1, slots=2, sets=1, accs=1, relayed=True, x_stages=4, w_stages=2),
 }
 TILE_RING = 32
 
 
-def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages, w_stages, late=0.2):
+def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stages, late=0.2):
     rng = random.Random(seed)
     steps_of_pair = 2 // blocks
-    x_of_step = 1 if joint else 2
     stride, mine = (sets, 1) if blocks == 2 else (1, 2 // sets)
 
     def bars(n, count=1):
@@ -51,7 +50,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages,
 
     w_full, w_empty = bars(w_stages), bars(w_stages, 1 if blocks == 2 else sets)
     x_full, step_full, step_empty = bars(x_stages), bars(slots), bars(slots)
-    x_empty = step_empty if joint and not relayed else bars(x_stages)
+    x_empty = bars(x_stages) if relayed else step_empty
     acc_full, acc_empty = bars(accs), bars(accs)
     w, x, a, acc = [None] * w_stages, [None] * x_stages, [None] * slots, [None] * accs
     tile = [None] * TILE_RING
@@ -75,7 +74,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages,
     def rows():
         ring = Ring(x_stages)
         for k in range(tiles):
-            for b in range(x_of_step * steps_of_pair * pairs):
+            for b in range(steps_of_pair * pairs):
                 while not x_empty[ring.slot].complete(ring.parity ^ 1):
                     yield False
                 slot, what = ring.slot, (k, b)
@@ -86,7 +85,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages,
     def convert(which):
         ahead = which if blocks == 2 else 0
         wr, s, xr = Ring(w_stages, ahead), Ring(slots, which), Ring(x_stages, which)
-        second = False
+        fresh = slots // sets
         for k in range(tiles):
             if k > 0 and ahead < pairs:
                 while not w_full[wr.slot].complete(wr.parity):
@@ -99,19 +98,19 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages,
                 for i in range(mine):
                     while not step_empty[s.slot].complete(s.parity ^ 1):
                         yield False
-                    if relayed and second:
+                    if fresh:
+                        fresh -= 1
+                    elif relayed:
                         x_empty[(xr.slot + slots) % x_stages].arrive()
-                    second = True
                     assert a[s.slot] is None, "a step overwritten"
                     yield True
                     number = ahead * steps_of_pair + (i if blocks == 1 else 0)
                     a[s.slot] = (k, number)
                     if i == mine - 1:
                         w_empty[wr.slot].arrive()
-                    if joint:
-                        while not x_full[xr.slot].complete(xr.parity):
-                            yield False
-                        assert x[xr.slot] == (k, number), "rows not there, or overwritten"
+                    while not x_full[xr.slot].complete(xr.parity):
+                        yield False
+                    assert x[xr.slot] == (k, number), "rows not there, or overwritten"
                     step_full[s.slot].arrive()
                     s.step(sets)
                     xr.step(sets)
@@ -132,29 +131,20 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, joint, relayed, x_stages,
                 if b == 0 and k > 0:
                     assert tile[k % TILE_RING] == k, "a tile's description overwritten"
                 assert a[s.slot] == (k, b), "a step not there"
-                for h in range(x_of_step):
-                    if not joint:
-                        while not x_full[xr.slot].complete(xr.parity):
-                            yield False
-                    assert x[xr.slot] == (k, b * x_of_step + h), "rows not there"
-                    slot, xslot, aslot = s.slot, xr.slot, ar.slot
-                    last = h == x_of_step - 1
-                    end = last and b == steps_of_pair * pairs - 1
+                assert x[xr.slot] == (k, b), "rows not there"
+                slot, xslot, aslot, end = s.slot, xr.slot, ar.slot, b == steps_of_pair * pairs - 1
 
-                    def finish(slot=slot, xslot=xslot, aslot=aslot, last=last, end=end, k=k, b=b, h=h):
-                        assert x[xslot] == (k, b * x_of_step + h) and a[slot] == (k, b), "operands changed under the MMAs"
-                        if not joint:
-                            x_empty[xslot].arrive()
-                        if last:
-                            a[slot] = None
-                            step_empty[slot].arrive()
-                        if end:
-                            acc[aslot] = k
-                            acc_full[aslot].arrive()
+                def finish(slot=slot, xslot=xslot, aslot=aslot, end=end, k=k, b=b):
+                    assert x[xslot] == (k, b) and a[slot] == (k, b), "operands changed under the MMAs"
+                    a[slot] = None
+                    step_empty[slot].arrive()
+                    if end:
+                        acc[aslot] = k
+                        acc_full[aslot].arrive()
 
-                    mmas.append(finish)
-                    xr.step()
-                    yield True
+                mmas.append(finish)
+                xr.step()
+                yield True
                 s.step()
             ar.step()
 
