@@ -14,12 +14,12 @@
 //                                                                 (a column's, over the rows)
 //
 // Both are bound by memory: 8 and 12 bytes a column, every input read once.  The forward takes a thread block a row, as
-// the norm in 8-bit rows does.
-// The gradient is persistent: a thread keeps eight columns and their column sums in registers while the rows pass, the
-// next row's loads in flight, so that the sums cost one FP32 row of each kind for a thread block at the end, and a second
-// small kernel adds those in a fixed order (no atomics: results do not change from run to run).  Rows of at most 2048
-// columns share a thread block, each by a group of warps; rows of more than 4096 are spread over a cluster of thread
-// blocks, whose warps write their sums into one another's shared memory.
+// the norm in 8-bit rows does: 16384 rows of 4096 in 86.5 us, 6.2 TB/s (0.93 of the measured copy rate), one token of 7168
+// columns in 3.1 us.
+// The gradient is persistent: a thread keeps eight columns and their column sums in registers while the rows pass, so that
+// the sums cost one FP32 row of each kind for a thread block at the end, and a second small kernel adds those in a fixed
+// order (no atomics: results do not change from run to run).  8192 rows of 4096 with every gradient take 70 us, 5.8 TB/s
+// (0.86); 1500 rows of 18432, over clusters, 76 us (0.65: 138 of 152 SMs have a thread block of six).
 #include <float.h>
 
 #include <map>
