@@ -22,9 +22,7 @@
 // (0.86); 1500 rows of 18432, over clusters, 76 us (0.65: 138 of 152 SMs have a thread block of six).
 #include <float.h>
 
-#include <map>
-#include <mutex>
-#include <tuple>
+#include <atomic>
 
 #include "kernels.h"
 #include "layer.h"
@@ -600,23 +598,25 @@ size_t block_norm_grad_workspace(int b, int H) {
 
 namespace {
 
-// The clusters of a launch that fit the current device at once, asked once for each kernel, shape and device: clusters lie
-// within a part of the GPU, so that there are fewer of some sizes than the SMs divided by their size.
+// The clusters of a launch that fit the current device at once: they lie within a part of the GPU, so that there are fewer
+// of some sizes than the SMs divided by their size.  With one thread block an SM that depends on the size and the device
+// alone, and is asked once for each.
 int clusters_at_once(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster) {
-  static std::mutex m;
-  static std::map<std::tuple<const void*, int, unsigned, size_t, int>, int> known;
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  std::lock_guard<std::mutex> lock(m);
-  int& found = known[{kernel, dev, cfg.blockDim.x, cfg.dynamicSmemBytes, cluster}];
-  if (found == 0) {
-    cudaLaunchConfig_t only = cfg;  // without the other attribute
-    only.attrs = cfg.attrs + 1;
-    only.numAttrs = 1;
-    found = cudaOccupancyMaxActiveClusters(&n, kernel, &only) == cudaSuccess && n > 0 ? n : 1;
+  const bool kept = dev < kDevices;
+  if (kept && (n = known[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchConfig_t only = cfg;  // without the other attribute
+  only.attrs = cfg.attrs + 1;
+  only.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &only) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
+    return 1;
   }
-  return found;
+  if (kept) known[dev][cluster].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 template <bool POST, bool CHANNEL>
