@@ -353,3 +353,37 @@ def test_in_graphs_that_share_a_workspace_and_on_a_side_stream(H):
         step(d, results[0])
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(results[0][k], wants[0][k]) for k in wants[0])
+
+
+@pytest.mark.parametrize("size", [1e-19, 1e19, 1e30])
+@pytest.mark.parametrize("H", [520, 4104, 9000])
+def test_gradients_of_rows_whose_squares_leave_the_range(size, H):
+    # rstd is that of the row as it was; with d_y near one every gradient is a number of FP32's range
+    g = gen(11)
+    d = inputs(g, 7, H, True, True, True)
+    d["x"] = (d["x"].float() * size).to(BF)
+    d_y, d_out = normal(g, 7, H), normal(g, 7, H)
+    if size < 1:
+        d["residual"].zero_()
+        d["token_gate"] += 1.0
+    got = backward(d, d_y, d_out, forward(d, eps=0.0)[2])
+    check_grad(d, d_y, d_out, got, eps=0.0)
+
+
+def test_gradients_at_once_on_several_streams():
+    g = gen(12)
+    calls = []
+    for b, H in ((400, 1032), (300, 4104), (200, 9000), (90, 20000)):
+        d = inputs(g, b, H, True, True, True)
+        calls.append((d, normal(g, b, H), normal(g, b, H), forward(d)[2]))
+    wants = [backward(*c) for c in calls]
+    streams, got = [torch.cuda.Stream() for _ in calls], [[] for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, stream, results in zip(calls, streams, got):
+            with torch.cuda.stream(stream):
+                results.append(backward(*c))
+    torch.cuda.synchronize()
+    for want, results in zip(wants, got):
+        assert all(torch.equal(r[k], want[k]) for r in results for k in want)
+    assert mt.moe_tail_take_device_error() == 0

@@ -138,3 +138,19 @@ def test_layer_in_a_graph():
         graph.replay()
     assert torch.equal(out, want)
     assert mt.moe_tail_take_device_error() == 0
+
+
+@pytest.mark.parametrize("finalize", [True, False])
+def test_a_token_with_one_expert_several_times(finalize):
+    g = gen(5)
+    b, E, K, H, I = 9, 4, 3, 264, 136
+    m = make(g, b, E, K, H, I, 64, True, finalize)
+    x, residual, out = normal(g, b, H), normal(g, b, H), torch.empty((b, H), dtype=BF, device="cuda")
+    ids, w = routes(g, b, K, E, local=1.0)
+    ids[0], ids[1, 1], ids[2], ids[3, 0] = 2, ids[1, 0], E, 10 ** 9  # all one, two alike, none here
+    _, _, want = plain(m, x, residual, None, ids, w)
+    m.norm(x, residual)
+    m.experts(ids, w, out)
+    off = (out.to(F64) - want).norm(dim=1)
+    assert (off <= 5e-3 * want.norm(dim=1) + 1e-6).all()
+    assert mt.moe_tail_take_device_error() == 0

@@ -318,3 +318,26 @@ def test_large_rows():
     for rows in (slice(0, 2), slice(R - 3, R)):
         check(out[rows], x[rows], weight, None, False)
     assert not out[1:R - 3].any()
+
+
+def test_calls_at_once_on_several_streams():
+    # every kind of tile on streams of their own, whose kernels share the SMs and their tensor memory
+    g = gen(13)
+    calls = []
+    for R, E, D, N, gated in ((1, 1, 2048, 264, True), (512, 64, 1024, 520, False), (300, 4, 1032, 776, True), (6000, 8, 392, 2056, False)):
+        weight = Weight(g, E, 2 * N if gated else N, D, 64)
+        counts = [R // E] * E
+        calls.append((normal(g, R, D), weight, offsets_of(counts) if E > 1 else None, gated))
+    wants = [call(*c) for c in calls]
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in wants]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, out, stream in zip(calls, outs, streams):
+            with torch.cuda.stream(stream):
+                call(*c, out[i])
+    torch.cuda.synchronize()
+    for c, out, want in zip(calls, outs, wants):
+        assert all(torch.equal(o, want) for o in out)
+        check(want, *c)
+    assert mt.moe_tail_take_device_error() == 0
