@@ -35,7 +35,7 @@ constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
 constexpr int kTileRing = 32;             // tiles that the weights' warp has described: more than it can be ahead
 
 // The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them: two MMAs for the same rows, whose
-// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 82 us, 106 without).
+// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 80.5 us; 106 without when wide ones took 82).
 template <int NT_, bool WIDE_>
 struct Form {
   static constexpr int NT = NT_;
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     if (again) *again = row_tiles > 1;  // more than one row tile reads these weights
     return true;
   };
-  const int pairs = (a.blocks + 1) / 2;  // an odd last block has one of zeros beside it
+  // An odd last block has one of zeros beside it where a step takes both.
+  const int pairs = (a.blocks + 1) / 2, steps = kStepsOfPair == 1 ? pairs : a.blocks;
   auto give_up = [&](unsigned bit) {
     if (!*abort_ptr) raise_error(bit);
     *abort_ptr = 1;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     bool ok = true;
     Tile q;
     for (int64_t i = blockIdx.x; ok && tile_at(i, q); i += gridDim.x) {
-      for (int b = 0; b < kStepsOfPair * pairs; ++b, ++g, x.step(kXStages)) {
+      for (int b = 0; b < steps; ++b, ++g, x.step(kXStages)) {
         if (!warp_wait(x_empty + 8 * x.slot, x.parity ^ 1u, abort_ptr)) {
           if (lane == 0) give_up(kErrWaitEmpty);
           ok = false;
@@ -280,7 +281,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         q = s_tile[k % kTileRing];
       }
       const uint32_t idesc = idesc_bf16(128, (q.rows + 15) & ~15);
-      const int steps = kStepsOfPair * pairs;
       for (int b = 0; b < steps; ++b, s.step(kSlots), x.step(kXStages)) {
         if (!warp_wait(step_full + 8 * s.slot, s.parity, abort_ptr, limit)) {
           if (lane == 0) give_up(kErrWaitFull);
@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         uint4 v[4];  // words 4 t + i: columns 32 i + 8 t .. of a block
 #pragma unroll
         for (int step = 0; step < kStepsOfPair; ++step, s.step(kSlots, kSets), x.step(kXStages, kSets)) {
+          if (step > 0 && 2 * ahead + step >= a.blocks) break;
           const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemA + s.slot * kSlotColumns + sub * 64 * kBlocks;
 #pragma unroll
           for (int h = 0; h < 2 * kBlocks; ++h) {  // 64 columns
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           // only now: the stores have taken what the loads brought, so nothing of the slot is still being read
-          if (step == kStepsOfPair - 1 && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
+          if ((step == kStepsOfPair - 1 || 2 * ahead + 1 >= a.blocks) && lane == 0) mbar_arrive(w_empty + 8 * w.slot);
           // one warp of the set sees the rows arrive too, so that the MMA warp has one barrier to wait for
           if (sub == 0 && quarter == 0 && !warp_wait(x_full + 8 * x.slot, x.parity, abort_ptr)) {
             if (lane == 0) give_up(kErrWaitFull);

@@ -40,9 +40,11 @@ FORMS = {  # as product_i4_tiles.cu has them
 TILE_RING = 32
 
 
-def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stages, late=0.2):
+def run(tiles, row_blocks, seed, blocks, slots, sets, accs, relayed, x_stages, w_stages, late=0.2):
     rng = random.Random(seed)
     steps_of_pair = 2 // blocks
+    pairs = (row_blocks + 1) // 2
+    steps = row_blocks if blocks == 1 else pairs  # of a tile
     stride, mine = (sets, 1) if blocks == 2 else (1, 2 // sets)
 
     def bars(n, count=1):
@@ -74,7 +76,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stag
     def rows():
         ring = Ring(x_stages)
         for k in range(tiles):
-            for b in range(steps_of_pair * pairs):
+            for b in range(steps):
                 while not x_empty[ring.slot].complete(ring.parity ^ 1):
                     yield False
                 slot, what = ring.slot, (k, b)
@@ -95,7 +97,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stag
                 while not w_full[wr.slot].complete(wr.parity):
                     yield False
                 assert w[wr.slot] == (k, ahead), "weights not there, or overwritten"
-                for i in range(mine):
+                for i in range(min(mine, row_blocks - 2 * ahead)):
                     while not step_empty[s.slot].complete(s.parity ^ 1):
                         yield False
                     if fresh:
@@ -106,7 +108,7 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stag
                     yield True
                     number = ahead * steps_of_pair + (i if blocks == 1 else 0)
                     a[s.slot] = (k, number)
-                    if i == mine - 1:
+                    if i == mine - 1 or 2 * ahead + 1 >= row_blocks:
                         w_empty[wr.slot].arrive()
                     while not x_full[xr.slot].complete(xr.parity):
                         yield False
@@ -125,14 +127,14 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stag
             while not acc_empty[ar.slot].complete(ar.parity ^ 1):
                 yield False
             assert acc[ar.slot] is None
-            for b in range(steps_of_pair * pairs):
+            for b in range(steps):
                 while not step_full[s.slot].complete(s.parity):
                     yield False
                 if b == 0 and k > 0:
                     assert tile[k % TILE_RING] == k, "a tile's description overwritten"
                 assert a[s.slot] == (k, b), "a step not there"
                 assert x[xr.slot] == (k, b), "rows not there"
-                slot, xslot, aslot, end = s.slot, xr.slot, ar.slot, b == steps_of_pair * pairs - 1
+                slot, xslot, aslot, end = s.slot, xr.slot, ar.slot, b == steps - 1
 
                 def finish(slot=slot, xslot=xslot, aslot=aslot, end=end, k=k, b=b):
                     assert x[xslot] == (k, b) and a[slot] == (k, b), "operands changed under the MMAs"
@@ -184,11 +186,11 @@ def run(tiles, pairs, seed, blocks, slots, sets, accs, relayed, x_stages, w_stag
 
 
 @pytest.mark.parametrize("form", FORMS)
-@pytest.mark.parametrize("pairs", [1, 2, 3, 4, 7, 16])
-def test_every_role_finds_its_data(form, pairs):
+@pytest.mark.parametrize("row_blocks", [1, 2, 3, 4, 5, 8, 13, 14, 31, 32])
+def test_every_role_finds_its_data(form, row_blocks):
     for seed in range(6):
         for late in (0.05, 0.5, 0.9):
-            run(1 + 150 // pairs, pairs, seed, late=late, **FORMS[form])
+            run(1 + 300 // row_blocks, row_blocks, seed, late=late, **FORMS[form])
 
 
 def test_the_model_sees_a_weight_ring_that_sets_do_not_share_evenly():
@@ -196,4 +198,4 @@ def test_the_model_sees_a_weight_ring_that_sets_do_not_share_evenly():
     bad = dict(FORMS["16 and 32 rows"], slots=9, x_stages=18, w_stages=4)
     with pytest.raises(AssertionError):
         for seed in range(200):
-            run(30, 7, seed, late=0.9, **bad)
+            run(30, 14, seed, late=0.9, **bad)

@@ -166,7 +166,7 @@ def test_weights_that_stream(R, E, D, N, gated):
 
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("R,E,D,N,group", [(3000, 8, 1024, 1288, 128), (5000, 2, 392, 2056, 64), (2600, 1, 2056, 2568, 32),
-                                           (9000, 60, 264, 1416, 32), (4100, 3, 640, 1800, 64)])
+                                           (9000, 60, 264, 1416, 32), (4100, 3, 640, 1800, 64), (6000, 4, 72, 2568, 32)])
 def test_many_rows(R, E, D, N, group, gated):
     # enough tiles for the wide ones, experts with one row tile and with many
     g = gen(R)
