@@ -35,7 +35,8 @@ constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
 constexpr int kTileRing = 32;             // tiles that the weights' warp has described: more than it can be ahead
 
 // The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them: two MMAs for the same rows, whose
-// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 80.5 us; 106 without when wide ones took 82).
+// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 80.5 us, without
+// 106).
 template <int NT_, bool WIDE_>
 struct Form {
   static constexpr int NT = NT_;
