@@ -390,11 +390,13 @@ int moe_tail_selftest_wait_timeout(unsigned int limit_us, void* stream);
 
 /* Failure-detection test hook (no counterpart on the pages): the limit of
  * the operand-stage waits -- the tensor-core issuer of the GEMM kernels and
- * of the 8-bit and 4-bit products waiting for a stage of weights and tokens, the staged
- * expert-TP finalize kernel's
- * threads waiting for a stage of route rows -- for calls made after it
- * returns (process-wide), in nanoseconds (1: give up at the first such
- * wait, whether or not the stage has landed); 0 restores the default (0.5 s).
+ * of the 8-bit and 4-bit products waiting for a stage of weights and tokens,
+ * the staged expert-TP finalize kernel's threads waiting for a stage of route
+ * rows, those of the norm gradient for rows above 2048 columns waiting for a
+ * row or for their cluster's sums -- for calls made after it returns
+ * (process-wide), in nanoseconds (1: give up at the first such wait, whether
+ * or not the stage has landed); 0 restores the default (0.5 s; the cluster's
+ * sums 1 s).
  * Only those waits change.  The waits that guard memory a CTA is about to
  * release keep their full limit: the copies still in flight when a call
  * aborts, and the tensor-core work issued before it, so an expired short wait

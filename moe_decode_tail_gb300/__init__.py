@@ -720,7 +720,8 @@ def moe_tail_set_kernel_form(call: int, form: int) -> None:
 
 def moe_tail_set_stage_wait_limit(limit_ns: int) -> None:
     """Failure-detection test hook: the operand-stage wait limit (ns) of the
-    GEMM and staged finalize kernels for later calls; 0 restores the default.
+    GEMM, staged finalize, product and wide norm-gradient kernels for later
+    calls; 0 restores the default.
     A limit shorter than a memory trip makes calls abort (device error bit 1)."""
     _check("moe_tail_set_stage_wait_limit", lib().moe_tail_set_stage_wait_limit(limit_ns))
 

@@ -18,16 +18,16 @@
 // columns in 3.1 us.
 // The gradient is persistent: a thread keeps eight columns and their column sums in registers while the rows pass, so that
 // the sums cost one FP32 row of each kind for a thread block at the end, and a second small kernel adds those in a fixed
-// order (no atomics: results do not change from run to run).  8192 rows of 4096 with every gradient take 70 us, 5.8 TB/s
-// (0.86); 1500 rows of 18432, over clusters, 76 us (0.65: 138 of 152 SMs have a thread block of six).
+// order (no atomics: results do not change from run to run).  8192 rows of 4096 with every gradient take 71 us, 5.7 TB/s
+// (0.85); 1500 rows of 18432, over clusters, 78 us (0.64: 138 of 152 SMs have a thread block of six).
 #include <float.h>
 
 #include <atomic>
 
 #include "kernels.h"
 #include "layer.h"
+#include "product.cuh"
 #include "rows.cuh"
-#include "tensor_core.cuh"
 
 namespace moetail {
 
@@ -388,15 +388,39 @@ __device__ __forceinline__ void st_async_f32x2(uint32_t addr, float a, float b, 
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Without an order of the memory accesses before it: does not wait for results on their way to memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned long long limit(const BlockNormGradArgs& a, int times) {
+  return a.stage_wait_ns ? a.stage_wait_ns : times * kWaitLimitNs;
+}
+
 // Wider rows: a row's (or a cluster's part of a row's) x, residual, d_y and d_residual_out arrive in shared memory, several
 // rows ahead, and each row has one barrier: the second sum of a row and the first of the next meet at it.  In a cluster the
 // warps send their sums to every thread block of it, and a barrier there counts their bytes: a barrier of the whole cluster
 // would also wait for the row's results on their way to memory (8192 columns: 5.5 us a row).
+//
+// Every wait is bounded in time.  A thread whose wait runs out raises a bit in the device error word, tells its cluster (so that
+// the others' waits end too) and asks for no more copies; what is written is undefined from there on.  Alone, a thread block
+// walks on without the rows, since its barriers count every warp.  In a cluster a warp to which a row's sums have not come
+// sends no more, and leaves.  No thread block ends before what is on its way to its shared memory has arrived: phases of
+// barriers that stayed open because some of their threads stopped earlier are completed first.
 template <bool POST, bool CHANNEL, bool CLUSTER>
 __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const BlockNormGradArgs a, const GradShape s) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float2 s_sum[2][kMaxCluster * kGradWarps];
   __shared__ __align__(8) uint64_t s_bar[8], s_sent[2];
+  __shared__ uint32_t s_abort;  // set in all thread blocks of a cluster
+  __shared__ int s_brought[4], s_sends[kGradWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = CLUSTER ? (int)cluster_rank() : 0, ranks = CLUSTER ? (int)cluster_size() : 1;
   const int64_t set = CLUSTER ? blockIdx.x / ranks : blockIdx.x;
@@ -406,6 +430,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
   if (threadIdx.x == 0) {
     for (int i = 0; i < s.stages; ++i) mbar_init(bars + 8 * i, tensors);
     for (int i = 0; i < 2; ++i) mbar_init(smem_addr(s_sent + i), 1);
+    s_abort = a.stage_wait_ns == 1;  // to give up whatever comes
+    if (s_abort) atomicOr(&g_norm_error, kErrWaitFull);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (CLUSTER) cluster_sync_all();  // its thread blocks have started, so that their shared memory can be written
@@ -437,13 +463,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
   Columns<POST, CHANNEL> columns;
   columns.load(a, first + v, live);
   Sums<POST, CHANNEL> sums;
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity)) atomicOr(&g_norm_error, kErrWaitFull);
+  // Both waits look at the barrier before anything else: what follows is for those that run out.
+  if (a.stage_wait_ns == 1) source = nullptr;
+  auto give_up = [&] {
+    if (!*(volatile uint32_t*)&s_abort) atomicOr(&g_norm_error, kErrWaitFull);
+    if (CLUSTER)
+      for (int i = 0; i < ranks; ++i) st_cluster_u32(map_to_rank(smem_addr(&s_abort), i), 1u);
+    else
+      *(volatile uint32_t*)&s_abort = 1u;
+    source = nullptr;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) {  // for a row
+    if (mbar_try_wait(bar, parity) || mbar_wait(bar, parity, limit(a, 1), &s_abort)) return;
+    give_up();
+  };
+  // One warp's sums of a row to all thread blocks of the cluster.
+  auto send = [&](int to, float x, float y) {
+    const uint32_t bar = smem_addr(s_sent + to);
+    if (threadIdx.x == 0) mbar_expect_tx(bar, 8u * ranks * s.warps);
+    if (lane < ranks)
+      st_async_f32x2(map_to_rank(smem_addr(&s_sum[to][part * kGradWarps + warp]), lane), x, y, map_to_rank(bar, lane));
   };
   // Two sums over the row, the same in every thread, in a fixed order; slots in turn as for the groups.
   int slot = 0;
   uint32_t sent_parity = 0;
+  bool lost = a.stage_wait_ns == 1;
   auto row_sums = [&](float x, float y) {
+    bool here = true;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -451,11 +497,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
     }
     if (CLUSTER) {
       // A warp sends again after it has read what came for this row, so that a slot is never overtaken.
+      send(slot, x, y);
+      // Longer than the others wait for a row before they send on without it.
       const uint32_t bar = smem_addr(s_sent + slot);
-      if (threadIdx.x == 0) mbar_expect_tx(bar, 8u * ranks * s.warps);
-      if (lane < ranks)
-        st_async_f32x2(map_to_rank(smem_addr(&s_sum[slot][part * kGradWarps + warp]), lane), x, y, map_to_rank(bar, lane));
-      wait(bar, sent_parity);
+      here = mbar_try_wait(bar, sent_parity) || mbar_wait(bar, sent_parity, limit(a, 2), &s_abort);
       if (slot == 1) sent_parity ^= 1u;
     } else {
       if (lane == 0) s_sum[slot][warp] = make_float2(x, y);
@@ -473,6 +518,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
       sum.y += __shfl_xor_sync(0xffffffffu, sum.y, off);
     }
     slot ^= 1;
+    if (CLUSTER && !here) {
+      give_up();
+      lost = true;
+    }
     return sum;
   };
   Values<POST, CHANNEL> w;  // of the row at hand
@@ -497,7 +546,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
   uint32_t stage = 0, parity = 0, at = mine;
   uint16_t *d_x = a.d_x + set * a.H + 8 * (first + v), *d_residual = a.d_residual + set * a.H + 8 * (first + v);
   float* d_token = a.d_token_gate && threadIdx.x == 0 && part == 0 ? a.d_token_gate + set : nullptr;
-  for (int k = 0; k < rows; ++k) {
+  int k = 0;
+  for (; k < rows; ++k) {
+    if (CLUSTER && __any_sync(0xffffffffu, lost)) break;  // after k + 1 rows' sums have been sent
     const uint4 d_out = a.d_residual_out ? ld_shared_v4(at + 3 * apart) : make_uint4(0, 0, 0, 0);
     float dot = w.inner(a, r, columns, sums, mean, ld_shared_v4(at + 2 * apart), d_out);
     if (!live) dot = 0.0f;
@@ -535,10 +586,52 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_staged_kernel(const Bloc
     mean = both.y * a.rcpH;
   }
   float* out = a.partial + set * 3 * a.H + 8 * (first + v);
-  if (!live) return;
-  if (POST && a.d_post_gamma) st_columns(out, sums.post);
-  if (a.d_pre_gamma) st_columns(out + a.H, sums.pre);
-  if (CHANNEL && a.d_channel_gate) st_columns(out + 2 * a.H, sums.channel);
+  if (live) {
+    if (POST && a.d_post_gamma) st_columns(out, sums.post);
+    if (a.d_pre_gamma) st_columns(out + a.H, sums.pre);
+    if (CHANNEL && a.d_channel_gate) st_columns(out + 2 * a.H, sums.channel);
+  }
+
+  // What is on its way to shared memory arrives before the thread block ends; where no wait ran out nothing is.
+  if (CLUSTER) {
+    together();
+    if (*(volatile uint32_t*)&s_abort) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the flags before the barrier
+    together();
+    cluster_sync_relaxed();
+  } else {
+    __syncthreads();
+  }
+  if (!s_abort) return;  // the same in all thread blocks of the cluster: nobody waits any more
+  const bool brings = lane == 0 && warp < tensors;
+  if (brings) s_brought[warp] = brought;
+  if (lane == 0) s_sends[warp] = k + 1;
+  together();
+  if (CLUSTER) cluster_sync_all();
+  else __syncthreads();
+  // A lane brings a row into a stage only once the stage's last one was complete, so that each stage lacks at most one
+  // arrival of a lane.
+  int most = 0;
+  for (int i = 0; i < tensors; ++i) most = max(most, s_brought[i]);
+  if (brings)
+    for (int i = brought; i < most; ++i) mbar_arrive(bars + 8 * (i % s.stages));
+  auto drain = [&](uint32_t bar, int round) {
+    if (!mbar_wait(bar, (uint32_t)round & 1u)) atomicOr(&g_norm_error, kErrWaitDrain);
+  };
+  if (threadIdx.x == 0)
+    for (int i = max(0, most - s.stages); i < most; ++i) drain(bars + 8 * (i % s.stages), i / s.stages);
+  if (CLUSTER) {
+    // A warp sends a row's sums only once all have sent the last row's: it lacks at most one row of those that most have.
+    together();
+    most = 0;
+    for (int i = lane; i < ranks * s.warps; i += 32)
+      most = max(most, (int)ld_cluster_u32(map_to_rank(smem_addr(&s_sends[i % s.warps]), i / s.warps)));
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (k + 1 < most) send((k + 1) & 1, 0.0f, 0.0f);
+    if (threadIdx.x == 0)
+      for (int i = max(0, most - 2); i < most; ++i) drain(smem_addr(s_sent + (i & 1)), i >> 1);
+    together();
+    cluster_sync_all();
+  }
 }
 
 // The sets' column sums added in their order: a warp takes every 32nd set for 128 columns, their loads in flight together.

@@ -88,6 +88,7 @@ struct BlockNormGradArgs {
   float *d_post_gamma, *d_pre_gamma, *d_channel_gate;  // [H] or null
   float* d_token_gate;                   // [b] or null
   float* partial;                        // workspace [row sets][3][H]
+  unsigned long long stage_wait_ns;      // of moe_tail_set_stage_wait_limit, 0: the default
 };
 cudaError_t launch_block_norm_grad(const BlockNormGradArgs& a, int sms, cudaStream_t stream);
 size_t block_norm_grad_workspace(int b, int H);

@@ -209,6 +209,7 @@ MOE_API int moe_tail_block_norm_grad(const void* d_y, const void* d_residual_out
   a.d_channel_gate = d_channel_gate;
   a.d_token_gate = d_token_gate;
   a.partial = static_cast<float*>(workspace);
+  a.stage_wait_ns = moetail::stage_wait_limit_ns();
   return finish(moetail::launch_block_norm_grad(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
