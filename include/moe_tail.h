@@ -593,10 +593,11 @@ size_t moe_tail_expert_product_workspace_bytes(int64_t rows, int num_experts, in
  *   W[e][n][k] = group_scale[e][n][k / group] * q[e][n][k],  q in [-8, 7]
  * for the rows r of [expert_offsets[e], expert_offsets[e + 1]).  Rows of no
  * expert are not written.  Every W is a BF16 number and every product exact in
- * FP32 (for |x| >= 2^-100; smaller ones lose bits, and a channel_scale of 2^112
- * or more may count as infinite: the sums are kept as multiples of 2^-15); the
- * sums are rounded as they grow, by at most (D + 256) * 2^-23 of the sum of
- * their terms' magnitudes.
+ * FP32 for |x| >= 2^-100 (smaller ones lose bits).  The sums are rounded as
+ * they grow, by at most (D + 256) * 2^-23 of the sum of their terms'
+ * magnitudes, and kept as multiples of 2^-15: a channel_scale of 2^112 or more
+ * may count as infinite, and so may a sum whose terms' magnitudes add up to
+ * 2^142 or more before the channel_scale, or to 2^128 or more with it.
  *   x          BF16 [rows][D]
  *   w          q in 4 bits, [num_experts][N][64 * ceil(D / 128)] bytes: a
  *              channel's columns in blocks of 128, sixteen 32-bit words

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) cs[j][h] = kUnscaled * __ldg(a.channel_scale + (int64_t)q.e * channels + channel(q, j, h));
+      for (int h = 0; h < 2; ++h) cs[j][h] = kScaled * __ldg(a.channel_scale + (int64_t)q.e * channels + channel(q, j, h));
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll

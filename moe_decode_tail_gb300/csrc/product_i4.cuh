@@ -30,16 +30,16 @@ struct Factors {
   __device__ static __nv_bfloat162 both(uint16_t bits) { return __bfloat162bfloat162(__ushort_as_bfloat16(bits)); }
 };
 
-// For q * 2^-6: 2^127, 2^123 and -8 * 2^-6.
-constexpr float kUnscaled = 64.0f;
-__device__ __forceinline__ Factors unscaled() { return Factors{Factors::both(0x7f00), Factors::both(0x7d00), Factors::both(0xbe00)}; }
+// Both kernels keep their sums as multiples of 2^-15, so that a row has the same range in either.
+constexpr float kScaled = 32768.0f;
+// For q * 2^-15: 2^118, 2^114 and -8 * 2^-15.
+__device__ __forceinline__ Factors unscaled() { return Factors{Factors::both(0x7a80), Factors::both(0x7880), Factors::both(0xb980)}; }
 
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(byte & 0xffu), __NV_E4M3)));
 }
 
 // For q * gs * 2^-15: gs * 2^118, gs * 2^114 and -8 gs * 2^-15 (gs has four significant bits and is below 2^9).
-constexpr float kScaled = 32768.0f;
 __device__ __forceinline__ Factors scaled(uint32_t e4m3) {
   const float gs = e4m3_value(e4m3);
   const __nv_bfloat162 v = __floats2bfloat162_rn(gs, gs);
