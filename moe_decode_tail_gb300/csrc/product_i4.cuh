@@ -60,14 +60,15 @@ __device__ __forceinline__ void int4x8_to_bf16(uint32_t word, const Factors& f, 
 // silu(g) * up.  With e = exp(-|g| / 2) the divisor is 1 + e^2; for g < 0 the fraction is multiplied by e^2 above and
 // below, one e with each factor, so that nothing leaves FP32's range before the result does.  The exponent of two, rounded to
 // FP32, and what the rounding left of it, which multiplies the power of two by 1 + (rest) ln 2: one rounded exponent would be
-// off by up to |g| units.
+// off by up to |g| units.  Powers below FP32's normal numbers are kept: a large up brings the result back into range down to
+// gates of -180.
 __device__ __forceinline__ float silu_times(float g, float up) {
   constexpr float kHalfLog2e = 0.72134752f, kBeyond = (float)(0.72134752044448170368 - (double)0.72134752f);
   constexpr float kLn2 = 0.69314718f;
-  const float m = fminf(fabsf(g), 512.0f), t = -kHalfLog2e * m;  // from 300 on the power is zero
+  const float m = fminf(fabsf(g), 512.0f), t = -kHalfLog2e * m;  // from 208 on the power is zero
   const float rest = fmaf(-kBeyond, m, fmaf(-kHalfLog2e, m, -t));
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
   e = fmaf(e, rest * kLn2, e);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, e, 1.0f)));
   const float p = g < 0.0f ? e : 1.0f;

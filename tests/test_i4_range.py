@@ -1,7 +1,8 @@
-"""The 4-bit products where a row or a sum is near the ends of FP32's range although the result is an ordinary number.
+"""The 4-bit products where a row, a sum or a gate is near the ends of FP32's range although the result is an ordinary number.
 
 Tolerances: a row with one column, or with a whole number of equal ones, has sums that are exact in FP32 and results that are
-BF16 numbers: equal bits are asked."""
+BF16 numbers: equal bits are asked.  silu's results round once (2^-8 of the value), and the exponential of half a gate, of
+which two are multiplied, is off by up to half of 2^-149 where it is below 2^-126: 2^-18 of itself for the gates here."""
 import pytest
 import torch
 
@@ -41,3 +42,19 @@ def test_rows_near_the_ends_of_the_range(size, q, gs, cs, columns, group, R, N):
     want = torch.tensor(size * q * gs * cs * columns, dtype=F64).to(BF).item()
     assert want == size * q * gs * cs * columns  # a BF16 number
     assert (out == want).all(), (out.flatten()[0].item(), want)
+
+
+@pytest.mark.parametrize("R,N", FORMS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gates_whose_silu_only_a_large_up_brings_into_range(sign, R, N):
+    gates = torch.tensor([-100.0, -150.0, -170.0, -174.0, -175.0, -176.0, -178.0, -180.0], device="cuda").repeat(N // 8)
+    q = torch.zeros((2 * N, 128), dtype=I8, device="cuda")
+    q[:N, 0], q[N:, 1] = 1, 1
+    x = torch.zeros((R, 128), dtype=BF, device="cuda")
+    x[:, 0], x[:, 1] = 1.0, sign * 2.0 ** 100
+    out = product(x, q, torch.ones((2 * N, 1), device="cuda"), torch.cat([gates, torch.full((N,), 2.0 ** 27, device="cuda")]), 128,
+                  gated=True)
+    z = gates.to(F64)
+    want = z / (1 + torch.exp(-z)) * (sign * 2.0 ** 127)
+    assert (want.abs() > 2.0 ** -126).all()
+    assert ((out.to(F64) - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -8) * want.abs()).all(), (out[0, :8], want[:8])
