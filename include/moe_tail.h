@@ -490,7 +490,10 @@ int moe_tail_block_norm(const void* x, const void* residual, const void* post_ga
  *                     d_residual_out
  *   d_post_gamma, d_pre_gamma, d_channel_gate   FP32 [H] or NULL (not wanted),
  *                     16-byte aligned: sums over the rows, in an order that
- *                     depends on b, H and the GPU's number of SMs alone
+ *                     depends on b, H and the GPU alone (its number of SMs
+ *                     and, above 4096 columns, how many clusters of thread
+ *                     blocks fit it at once, which two GPUs with as many SMs
+ *                     need not have alike)
  *   d_token_gate      FP32 [b] or NULL
  *   workspace         >= moe_tail_block_norm_grad_workspace_bytes(b, H) bytes,
  *                     16-byte aligned; one for b rows serves fewer

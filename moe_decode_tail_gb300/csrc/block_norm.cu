@@ -694,22 +694,20 @@ namespace {
 // The clusters of a launch that fit the current device at once: they lie within a part of the GPU, so that there are fewer
 // of some sizes than the SMs divided by their size.  With one thread block an SM that depends on the size and the device
 // alone, and is asked once for each.
-int clusters_at_once(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster) {
+cudaError_t clusters_at_once(const void* kernel, const cudaLaunchConfig_t& cfg, int cluster, int* n) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices][kMaxCluster + 1];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   const bool kept = dev < kDevices;
-  if (kept && (n = known[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
+  if (kept && (*n = known[dev][cluster].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
   cudaLaunchConfig_t only = cfg;  // without the other attribute
   only.attrs = cfg.attrs + 1;
   only.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &only) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    return 1;
-  }
-  if (kept) known[dev][cluster].store(n, std::memory_order_relaxed);
-  return n;
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &only);
+  if (e == cudaSuccess && kept) known[dev][cluster].store(*n, std::memory_order_relaxed);
+  return e;
 }
 
 template <bool POST, bool CHANNEL>
@@ -748,13 +746,17 @@ cudaError_t launch_grad(const BlockNormGradArgs& a, int most, int* sets, cudaStr
     // with five, 90 with six).  At least a warp for each tensor of a row.
     for (int c = s.cluster + s.cluster % 2; c <= kMaxCluster && a.H >= 8 * 32 * 4 * c; c += 2) {
       shape(c);
-      const int fit = clusters_at_once((const void*)kernel, cfg, c), n = fit < most / c ? fit : most / c;
+      int fit = 0;
+      const cudaError_t e = clusters_at_once((const void*)kernel, cfg, c, &fit);
+      if (e != cudaSuccess) return e;  // another number would be another order of the sums
+      const int n = fit < most / c ? fit : most / c;
       if (n * c > best_blocks) {
         best = c;
         best_blocks = n * c;
         at_once = n;
       }
     }
+    if (best_blocks == 0) return cudaErrorLaunchOutOfResources;  // no size fits
     shape(best);
   }
   s.row_sets = *sets = row_sets(a.b, s.groups, at_once);
