@@ -637,6 +637,15 @@ int moe_tail_gated_product_i4(const void* x, const void* w, const void* group_sc
                               const int32_t* expert_offsets, int64_t rows, int num_experts, int I, int D,
                               int group, void* out, void* stream);
 
+/*
+ * Rows of a tile that the 4-bit products take for these sizes on the current
+ * device (gated: 0 or 1): 8 is the kernel for few rows, 128 the wide tiles,
+ * between them are the others' 16, 32 and 64.  0 where the products refuse
+ * the sizes.  The results do not tell; tests ask, so that they keep to the
+ * form that they are for.
+ */
+int moe_tail_product_i4_tile_rows(int64_t rows, int num_experts, int N, int D, int gated);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,7 +26,7 @@ __all__ = [
     "moe_tail_sort_workspace_bytes", "moe_tail_dispatch_rows", "moe_tail_combine_rows", "moe_tail_combine_grad",
     "moe_tail_expert_product", "moe_tail_expert_product_workspace_bytes", "moe_tail_block_norm",
     "moe_tail_block_norm_grad", "moe_tail_block_norm_grad_workspace_bytes", "moe_tail_expert_product_i4",
-    "moe_tail_gated_product_i4",
+    "moe_tail_gated_product_i4", "moe_tail_product_i4_tile_rows",
 ]
 
 OK, EINVAL, ECUDA, ENOTSUP = 0, 1, 2, 3
@@ -102,6 +102,7 @@ def lib() -> ctypes.CDLL:
         L.moe_tail_block_norm_grad_workspace_bytes.restype = sz
         L.moe_tail_expert_product_i4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
         L.moe_tail_gated_product_i4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i32, P, P]
+        L.moe_tail_product_i4_tile_rows.argtypes = [i64, i32, i32, i32, i32]
         for name in ("moe_tail_ep_finalize", "moe_tail_tp_finalize", "moe_tail_latent_up", "moe_shared_expert",
                      "moe_tail_norm_quant", "moe_tail_silu_quant", "moe_tail_sort_routes", "moe_tail_dispatch_rows",
                      "moe_tail_combine_rows", "moe_tail_combine_grad", "moe_tail_expert_product",
@@ -110,7 +111,8 @@ def lib() -> ctypes.CDLL:
                      "moe_tail_latent_up_flags", "moe_tail_ep_finalize_flags", "moe_tail_tp_finalize_flags",
                      "moe_tail_set_kernel_form", "moe_tail_set_stage_wait_limit",
                      "moe_tail_up_project_shared_down", "moe_shared_down_persistent", "moe_tail_block_norm",
-                     "moe_tail_block_norm_grad", "moe_tail_expert_product_i4", "moe_tail_gated_product_i4"):
+                     "moe_tail_block_norm_grad", "moe_tail_expert_product_i4", "moe_tail_gated_product_i4",
+                     "moe_tail_product_i4_tile_rows"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -698,6 +700,12 @@ def moe_tail_gated_product_i4(x, w, group_scale, channel_scale, out, *, group, e
     """out (BF16 [rows, I]) = silu(gate) * up in one kernel, gate and up the first and last I channels of that product
     with a weight of 2 I channels (arguments as for moe_tail_expert_product_i4)."""
     return _product_i4("moe_tail_gated_product_i4", x, w, group_scale, channel_scale, out, group, expert_offsets, 2, stream)
+
+
+def moe_tail_product_i4_tile_rows(rows: int, num_experts: int, N: int, D: int, *, gated: bool = False) -> int:
+    """Rows of a tile that the 4-bit products take for these sizes: 8 (the kernel for few rows), 16, 32, 64 or 128 (wide
+    tiles); 0 where they refuse the sizes.  N: channels of the result."""
+    return int(lib().moe_tail_product_i4_tile_rows(rows, num_experts, N, D, int(bool(gated))))
 
 
 def moe_tail_status_str(status: int) -> str:

@@ -470,3 +470,8 @@ MOE_API int moe_tail_gated_product_i4(const void* x, const void* w, const void* 
                                       void* out, void* stream) {
   return product_i4(x, w, group_scale, channel_scale, expert_offsets, rows, num_experts, I, D, group, true, out, stream);
 }
+
+MOE_API int moe_tail_product_i4_tile_rows(int64_t rows, int num_experts, int N, int D, int gated) {
+  if (!i4_sizes_ok(rows, num_experts, N, D, 128)) return 0;
+  return moetail::product_i4_plan(rows, num_experts, N, D, gated != 0, device_sms()).rows;
+}
