@@ -229,18 +229,19 @@ class ExpertLayerI4(_ExpertLayer):
         self._h = new(torch.bfloat16, rows, I)
         self._workspace = new(torch.uint8, workspace)
 
-    def norm(self, x, residual, *, residual_out=None, token_gate=None, channel_gate=None):
+    def norm(self, x, residual, *, residual_out=None, token_gate=None, channel_gate=None, rstd=None):
         """x, the last block's output, normed with post_gamma, gated and added to the scaled residual (in place, or into
         residual_out), and the sum normed with gamma into the layer's rows.  Returns (the sum, those rows), BF16 [b, H]:
-        the rows are the router's input, and stay until the next norm()."""
+        the rows are the router's input, and stay until the next norm().  rstd (FP32 [b, 2]) receives what
+        moe_tail_block_norm_grad takes; its x and residual are those of before the call, so residual_out is one's own then."""
         b = self._tokens(x)
         if residual_out is None:
             residual_out = residual
         self._normed = None
         y = self._y[:b]
         moe_tail_block_norm(x, residual, self.post_gamma, self.gamma, residual_out, y, token_gate=token_gate,
-                            channel_gate=channel_gate, residual_scale=self.residual_scale, gain_center=self.gain_center,
-                            eps=self.eps)
+                            channel_gate=channel_gate, rstd=rstd, residual_scale=self.residual_scale,
+                            gain_center=self.gain_center, eps=self.eps)
         self._normed = b
         return residual_out, y
 
