@@ -14,7 +14,7 @@
 //                                                                 (a column's, over the rows)
 //
 // Both are bound by memory: 8 and 12 bytes a column, every input read once.  The forward takes a thread block a row, as
-// the norm in 8-bit rows does: 16384 rows of 4096 in 86.5 us, 6.2 TB/s (0.93 of the measured copy rate), one token of 7168
+// the norm in 8-bit rows does: 16384 rows of 4096 in 86.2 us, 6.2 TB/s (0.93 of the measured copy rate), one token of 7168
 // columns in 3.1 us.
 // The gradient is persistent: a thread keeps eight columns and their column sums in registers while the rows pass, so that
 // the sums cost one FP32 row of each kind for a thread block at the end, and a second small kernel adds those in a fixed

@@ -9,7 +9,8 @@
 // Most calls take the tiles of product_i4_tiles.cu.  Here is the kernel for at most eight rows and too few tiles to occupy
 // the SMs: one dense weight and a token or a few.  A thread block takes 32 channels, its eight warps a block of 128 columns
 // each, as mma.sync operands made in registers; two copies bring a step of 1024 columns, weights and rows, so that the first
-// bytes are asked for at once and latency is what is left: one token by 7168 x 3584 takes 7.2 us, 1.8 TB/s of packed weights
+// bytes are asked for at once and latency is what is left: one token by 7168 x 3584 takes 7.2 us on the device (a call from
+// Python 8), 1.8 TB/s of packed weights
 // (24 copies a step took 8.2, the tiles 9.3).  Wider, the tiles are faster (one token by 12288 x 4096: 11.1 us, 11.8 here).
 #include "kernels.h"
 #include "layer.h"
@@ -316,9 +317,13 @@ ProductI4Plan product_i4_plan(int64_t R, int E, int N, int D, bool gated, int sm
   p.tiles = want > kRows || hit * ((N + 127) / 128) * (gated ? 2 : 1) >= sms / 2 || E > kMostExperts;
   p.wide = false;
   if (p.tiles) {
-    // Wide tiles pay from 128 rows an expert on, where there is one for each SM: 60 experts of 1408 x 2048 with 68 rows each
-    // take 43 us in wide tiles and 35 in tiles of 64, with 137 each 58 and 54, gated 98 and 101; 128 with 256 each of 4096
-    // x 2048 389 and 560.  One expert's 1024 rows by 4096 x 4096 (128 wide tiles) take 36 us in tiles of 64.
+    // Wide tiles pay from about 128 rows an expert on, where there is one for each SM, by 10 to 20%: 128 experts of 4096 x 2048
+    // with 256 rows each take 421 us in wide tiles and 520 in tiles of 64, with 137 each 270 and 320; 60 of 1408 x 2048 with
+    // 192 each 63 and 71, gated 114 and 135.  Near the border it depends on how the tiles fill the rounds: those 60 with 137
+    // rows each 58 and 56.5, gated 98 and 109; 8 of 4096 x 4096 with 160 each 49 and 53.5, with 129 51 and 39.  The rows
+    // counted are the buffer's: where an eighth of them have an expert here (512 tokens x 8 routes, 16 experts of 128), wide
+    // ones take 23 us and the others 21 (gated 1024 x 4096), 15 and 13 (4096 x 1024).  One expert's 1024 rows by 4096 x 4096
+    // (128 wide tiles) take 35 us in tiles of 64 and would take 28.5.
     const int64_t row_tiles = E == 1 ? (R + 127) / 128 : R / 128 + hit;  // of a wide tile's rows
     p.wide = want > kWideFrom && row_tiles * ((N + 255) / 256) * (gated ? 2 : 1) >= sms;
     p.rows = p.wide ? 128 : want <= 16 ? 16 : want <= 32 ? 32 : 64;

@@ -10,12 +10,13 @@
 // and meet in shared memory; a wide one has an accumulator for each, and a thread both factors of a result.
 //
 // With few rows the weights' way from memory is the bound, and before it what a step costs the warps that issue MMAs and that
-// convert.  64 tokens x 8 routes over 128 experts of 2048 x 4096 take 93 us (0.54 GB, 0.88 of the measured copy rate), of
+// convert.  64 tokens x 8 routes over 128 experts of 2048 x 4096 take 93 us (0.54 GB, 0.87 of the measured copy rate), of
 // 4096 x 1024 with groups of 32 columns 58 us (0.74).  On the way there: a block a step with two barriers and commits 180 us;
 // a pair a step, one barrier and one commit 112; three sets of converting warps that take whole steps instead of two that
 // share them 102; rows asked for further ahead 100; tiles found by one warp for those that have no time to 94.
 // With many rows the MMAs are the bound, with A in tensor memory about a third slower than their operations: 32768 rows over
-// 128 experts of 4096 x 2048 take 389 us, 1.41 PFLOP/s (0.74 of a library BF16 product; 430 on a box with a lower clock).
+// 128 experts of 4096 x 2048 take 390 to 440 us, as the GPU's clock under that load is, 1.25 to 1.41 PFLOP/s (0.65 to 0.74 of a
+// library BF16 product).
 //
 // Every wait is bounded in time; on expiry the kernel raises a bit in the device error word, lets its copies and MMAs
 // finish, frees its tensor memory and returns.
@@ -35,7 +36,7 @@ constexpr int kStaging = kRun * 128 * 4;  // of an epilogue set
 constexpr int kTileRing = 32;             // tiles that the weights' warp has described: more than it can be ahead
 
 // The forms of a tile: NT rows by 128 stored channels, or, wide, 128 rows by 256 of them: two MMAs for the same rows, whose
-// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 80.5 us, without
+// way from L2 is halved (1999 tokens x 6 routes, half of them here, over 60 gated experts of 2832 x 2056: 82 us, without
 // 106).
 template <int NT_, bool WIDE_>
 struct Form {
